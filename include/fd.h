@@ -306,6 +306,171 @@ fd_status fd_decode_static(const fd_desc* desc, const void* q, const void* k_cac
                            const void* v_cache, const int32_t* seqlens,
                            const int32_t* block_table, void* out, float* lse, void* stream);
 
+/* ======================================================================
+ * The serving step around a decode: page tables, the prompt's attention, the
+ * store into an 8-bit cache with fine scales, and the decode over it.  The
+ * conventions at the head of this file hold (ownership, streams, errors, no
+ * allocation, no synchronisation, CUDA-graph capturable); conditions only the
+ * GPU can see are recorded in the device status word.
+ * ====================================================================== */
+
+/* Scales of an FD_E4M3 cache, one per (block of tokens, KV head), for K and V:
+ * token t of KV head g in page P (paged) or sequence b (contiguous) stands for
+ *     stored * k[P*k_stride_b + g*k_stride_h + (t / block)*k_stride_n]
+ * with t counted within the page (paged) or the sequence (contiguous).
+ * Strides in elements, >= 0.  fd_decode_scaled reads any non-negative finite
+ * scales; fd_cache_store writes powers of two.
+ * block: a power of two, 1 <= block <= 1024; paged: at most page_size. */
+typedef struct fd_kv_scales {
+    float* k;                   /* device */
+    float* v;                   /* device */
+    int64_t k_stride_b, k_stride_h, k_stride_n;
+    int64_t v_stride_b, v_stride_h, v_stride_n;
+    int32_t block;              /* tokens per scale */
+    int32_t reserved;           /* must be 0 */
+} fd_kv_scales;
+
+/* fd_decode over an FD_E4M3 cache with block scales: key j of (b, g) is
+ * desc->k_scale * scale(j) * stored, value j likewise with desc->v_scale.
+ * desc, plan, workspace and results are those of fd_decode for desc->kv_dtype
+ * FD_E4M3 (other cache types: FD_ERR_INVALID_ARG); scales of blocks wholly
+ * past a sequence's end are never read.  What the cache and the scales hold
+ * for tokens past the end of a sequence does not matter, NaN included.  Within
+ * a query block the block's own tokens are taken as finite. */
+fd_status fd_decode_scaled(const fd_desc* desc, const fd_kv_scales* scales, const void* q,
+                           const void* k_cache, const void* v_cache, const int32_t* seqlens,
+                           const int32_t* block_table, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Rows to store: n_tokens rows of K and V per KV head, k_src at
+ * k + t*k_src_stride_t + g*k_src_stride_h (16-byte aligned rows), into an
+ * FD_E4M3 cache laid out like fd_desc's (batch: sequences of a contiguous one). */
+typedef struct fd_store_desc {
+    int32_t n_tokens;           /* >= 0; 0 enqueues nothing */
+    int32_t n_kv_heads;         /* >= 1 */
+    int32_t head_dim;           /* 128 */
+    int32_t src_dtype;          /* FD_F16 or FD_BF16 */
+    int64_t k_src_stride_t, k_src_stride_h, v_src_stride_t, v_src_stride_h;
+    int64_t k_stride_b, k_stride_h, k_stride_t;
+    int64_t v_stride_b, v_stride_h, v_stride_t;
+    int64_t kv_extent;          /* contiguous: tokens per sequence; paged: pages in the pool */
+    int32_t page_size;          /* 0 = contiguous; else a power of two >= 8 */
+    int32_t batch;              /* contiguous: sequences in the cache; paged: unused */
+} fd_store_desc;
+
+/* Stores new K/V rows into the cache, quantised to E4M3 with one power-of-two
+ * scale per (block of tokens, KV head).
+ *  slots  : device int64[n_tokens], row t's place: page*page_size + offset
+ *           (paged) or sequence*kv_extent + token (contiguous).  A negative slot
+ *           skips its row; one outside the cache skips it and sets
+ *           FD_ERR_DEVICE_BOUNDS in the status word.
+ * The rows that go to one block are adjacent in the list and in token order,
+ * as a step's ragged rows are (skipped rows between them keep their distance
+ * and leave their places as they are), and no slot appears twice (else which
+ * row a block keeps is unspecified).  With amax the largest finite |x| of a block's
+ * new rows, the scale they need is the smallest power of two s >= 2^-126 with
+ * amax <= 448 s.
+ *  - New rows that begin a block (row 0 of it) take that scale; what the block
+ *    and its scale held before counts for nothing (a recycled page).
+ *  - Rows behind others of their block use the larger of the block's scale and
+ *    the one they need.  If it grew, the rows before them in the block are
+ *    rewritten for it (exact but for values that become E4M3 subnormals).
+ * Each value is rounded once to the nearest E4M3 number of its block (ties to
+ * even); an infinity or NaN is stored as NaN.  Rows of the block behind the
+ * new ones are left as they are. */
+fd_status fd_cache_store(const fd_store_desc* desc, const fd_kv_scales* scales, const void* k,
+                         const void* v, const int64_t* slots, void* k_cache, void* v_cache,
+                         void* stream);
+
+#define FD_MAX_TABLE_BATCH 8192   /* sequences of one fd_page_tables call */
+
+typedef struct fd_page_desc {
+    int32_t batch;              /* sequences, 0 <= batch <= FD_MAX_TABLE_BATCH */
+    int32_t page_size;          /* tokens per page, a power of two >= 8 */
+    int32_t max_pages_per_seq;  /* row length of block_table */
+    int32_t n_pages;            /* pages in the pool */
+    int32_t n_free_max;         /* entries of free_pages */
+    int32_t n_slots;            /* entries of slots and positions */
+} fd_page_desc;
+
+/* Page tables and slot map of one step, on the GPU: sequence b holds
+ * seqlens[b] tokens and gets new_tokens[b] more (0 allowed).
+ *  seqlens, new_tokens : device int32[batch].
+ *  free_pages, free_count : device int32[n_free_max] and int32[1], a stack of
+ *                  free pages; pages are taken from its end.  The array itself
+ *                  is not written.
+ *  block_table   : device int32[batch*max_pages_per_seq]; the entries of the
+ *                  pages a sequence needs beyond ceil(seqlens[b]/page_size) are
+ *                  written, all others are left as they are.
+ *  seqlens_out, free_count_out : device, the lengths and the free count
+ *                  afterwards; each may be the input's own buffer.
+ *  cu_tokens     : device int32[batch+1] or NULL: cu_tokens[b] = the new tokens
+ *                  of the sequences before b.
+ *  slots         : device int64[n_slots]: for new token cu_tokens[b] + i the
+ *                  place (page*page_size + offset) of position seqlens[b] + i,
+ *                  as fd_cache_store takes it; -1 behind the last new token.
+ *  positions     : device int32[n_slots] or NULL: seqlens[b] + i; -1 behind.
+ * The i-th new page of the step, sequences in order, is
+ * free_pages[free_count - 1 - i].  A sequence whose new pages the free list
+ * cannot cover in that order gets none: its length stays, its slots are -1,
+ * and so it is with one whose length is negative, would pass
+ * max_pages_per_seq*page_size, or whose new tokens do not fit n_slots (a
+ * negative count is taken as 0).  Those, and a page index outside the pool
+ * (its slots are -1), set FD_ERR_DEVICE_BOUNDS in the status word. */
+fd_status fd_page_tables(const fd_page_desc* desc, const int32_t* seqlens,
+                         const int32_t* new_tokens, const int32_t* free_pages,
+                         const int32_t* free_count, int32_t* block_table, int32_t* seqlens_out,
+                         int32_t* free_count_out, int32_t* cu_tokens, int64_t* slots,
+                         int32_t* positions, void* stream);
+
+/* Whole prompts: packed sequences of different lengths.
+ * q   [total_q, n_q_heads, 128] at q + t*q_stride_t + h*q_stride_h, k and v
+ * [total_k, n_kv_heads, 128] likewise (16-byte aligned bases, strides multiples
+ * of 8 elements); rows cu_q[b] .. cu_q[b+1]-1 of q and cu_k[b] .. cu_k[b+1]-1 of k
+ * and v belong to sequence b. */
+typedef struct fd_prompt_desc {
+    int32_t batch;              /* sequences >= 0; 0 enqueues nothing */
+    int32_t n_q_heads;          /* >= 1 */
+    int32_t n_kv_heads;         /* >= 1, divides n_q_heads */
+    int32_t head_dim;           /* 128 */
+    int32_t dtype;              /* of q, k, v: FD_F16 or FD_BF16 */
+    int32_t out_dtype;          /* FD_F32, FD_F16 or FD_BF16 */
+    int64_t q_stride_t, q_stride_h;
+    int64_t k_stride_t, k_stride_h;
+    int64_t v_stride_t, v_stride_h;
+    int32_t total_q, total_k;   /* rows of q, and of k and v */
+    int32_t max_q, max_k;       /* the longest sequence's queries and keys as the host knows them;
+                                   0: total_q, total_k.  They plan the launch only: any values give
+                                   the same results up to rounding. */
+    int32_t causal;             /* 0: every query sees all keys of its sequence; 1: see fd_prompt */
+    int32_t n_splits;           /* key splits per query tile; <= 0: planned */
+    int32_t flags;              /* must be 0 */
+    int32_t reserved;           /* must be 0 */
+} fd_prompt_desc;
+
+/* Bytes of workspace fd_prompt needs for `desc` (0: none), 0 for an invalid one too. */
+size_t fd_prompt_workspace_size(const fd_prompt_desc* desc);
+
+/* Attention over whole prompts: for each sequence with nq queries and nk keys,
+ *     s_ij = q_i . k_j / sqrt(128),  out_i = sum_j softmax(s_i)_j v_j over the keys
+ *     query i sees,  lse_i = log sum_j exp(s_ij);  query head h reads KV head h / G.
+ * causal: the queries are the last nq of the nk positions, query i sees keys
+ * j <= i + nk - nq (a prompt's chunk behind keys that are there already has nk >
+ * nq).  A query that sees no key gets out = 0 and lse = -inf.
+ * A key's or value's infinities and NaN reach only the queries that see it.
+ *  cu_q, cu_k : device int32[batch+1], ascending, within [0, total_q] and
+ *               [0, total_k].  A sequence for which that does not hold is skipped
+ *               and sets FD_ERR_DEVICE_BOUNDS in the status word.
+ *  out        : device [total_q, n_q_heads, 128], out_dtype, contiguous.
+ *  lse        : device float[total_q*n_q_heads]; NULL to skip.
+ *  workspace  : device, >= fd_prompt_workspace_size(desc) bytes, 256-byte
+ *               aligned; NULL if that is 0.
+ * Rows of out and lse that belong to no sequence are left as they are.  For one
+ * query per sequence over a long cache fd_decode is the call. */
+fd_status fd_prompt(const fd_prompt_desc* desc, const void* q, const void* k, const void* v,
+                    const int32_t* cu_q, const int32_t* cu_k, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,7 +45,8 @@ LIB_PATH = _build.LIB_PATH
 # every function the header declares (checked against include/fd.h by the tests)
 EXPORTS = ("fd_abi_version", "fd_status_string", "fd_num_sms", "fd_plan_splits", "fd_plan",
            "fd_plan_desc", "fd_workspace_size", "fd_decode", "fd_split_states", "fd_combine_states",
-           "fd_device_status", "fd_decode_status", "fd_decode_static")
+           "fd_device_status", "fd_decode_status", "fd_decode_static", "fd_decode_scaled",
+           "fd_cache_store", "fd_page_tables", "fd_prompt", "fd_prompt_workspace_size")
 
 
 class FdDesc(ctypes.Structure):
@@ -70,6 +71,50 @@ class FdDesc(ctypes.Structure):
         d = FdDesc()
         ctypes.pointer(d)[0] = self
         return d
+
+
+class FdKvScales(ctypes.Structure):
+    """Mirror of ``fd_kv_scales`` (include/fd.h)."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_stride_b", ctypes.c_int64), ("k_stride_h", ctypes.c_int64), ("k_stride_n", ctypes.c_int64),
+        ("v_stride_b", ctypes.c_int64), ("v_stride_h", ctypes.c_int64), ("v_stride_n", ctypes.c_int64),
+        ("block", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class FdStoreDesc(ctypes.Structure):
+    """Mirror of ``fd_store_desc`` (include/fd.h)."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("src_dtype", ctypes.c_int32),
+        ("k_src_stride_t", ctypes.c_int64), ("k_src_stride_h", ctypes.c_int64),
+        ("v_src_stride_t", ctypes.c_int64), ("v_src_stride_h", ctypes.c_int64),
+        ("k_stride_b", ctypes.c_int64), ("k_stride_h", ctypes.c_int64), ("k_stride_t", ctypes.c_int64),
+        ("v_stride_b", ctypes.c_int64), ("v_stride_h", ctypes.c_int64), ("v_stride_t", ctypes.c_int64),
+        ("kv_extent", ctypes.c_int64), ("page_size", ctypes.c_int32), ("batch", ctypes.c_int32),
+    ]
+
+
+class FdPageDesc(ctypes.Structure):
+    """Mirror of ``fd_page_desc`` (include/fd.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "page_size", "max_pages_per_seq", "n_pages",
+                                              "n_free_max", "n_slots")]
+
+
+class FdPromptDesc(ctypes.Structure):
+    """Mirror of ``fd_prompt_desc`` (include/fd.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+        ("v_stride_t", ctypes.c_int64), ("v_stride_h", ctypes.c_int64),
+        ("total_q", ctypes.c_int32), ("total_k", ctypes.c_int32),
+        ("max_q", ctypes.c_int32), ("max_k", ctypes.c_int32),
+        ("causal", ctypes.c_int32), ("n_splits", ctypes.c_int32),
+        ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
 
 
 class FdError(RuntimeError):
@@ -112,6 +157,12 @@ def _load():
             "fd_device_status": (i32, [vp, i32]),
             "fd_decode_status": (i32, [vp]),
             "fd_decode_static": (i32, [dp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "fd_decode_scaled": (i32, [dp, ctypes.POINTER(FdKvScales), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "fd_cache_store": (i32, [ctypes.POINTER(FdStoreDesc), ctypes.POINTER(FdKvScales),
+                                     vp, vp, vp, vp, vp, vp]),
+            "fd_page_tables": (i32, [ctypes.POINTER(FdPageDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "fd_prompt_workspace_size": (sz, [ctypes.POINTER(FdPromptDesc)]),
+            "fd_prompt": (i32, [ctypes.POINTER(FdPromptDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -139,6 +190,10 @@ def _stream(s):
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _nbytes(x) -> int:
+    return 0 if x is None else x.numel() * x.element_size()
 
 
 def check(status: int, what: str = "") -> int:
@@ -236,6 +291,43 @@ def fd_decode_static(desc: FdDesc, q, k_cache, v_cache, seqlens, block_table, ou
                                         _stream(stream)))
 
 
+def fd_decode_scaled(desc: FdDesc, scales: FdKvScales, q, k_cache, v_cache, seqlens, block_table, out, lse,
+                     workspace, workspace_bytes: int | None = None, stream=None) -> int:
+    """fd_decode over an E4M3 cache with a scale per (block of tokens, KV head); see make_scales."""
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    return int(_load().fd_decode_scaled(ctypes.byref(desc), ctypes.byref(scales), _ptr(q), _ptr(k_cache),
+                                        _ptr(v_cache), _ptr(seqlens), _ptr(block_table), _ptr(out), _ptr(lse),
+                                        _ptr(workspace), int(wb), _stream(stream)))
+
+
+def fd_cache_store(desc: FdStoreDesc, scales: FdKvScales, k, v, slots, k_cache, v_cache, stream=None) -> int:
+    """New K/V rows into an E4M3 cache at `slots` (int64), quantised with a power-of-two
+    scale per (block of tokens, KV head); writes the cache and the scales."""
+    return int(_load().fd_cache_store(ctypes.byref(desc), ctypes.byref(scales), _ptr(k), _ptr(v), _ptr(slots),
+                                      _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+
+
+def fd_page_tables(desc: FdPageDesc, seqlens, new_tokens, free_pages, free_count, block_table, seqlens_out,
+                   free_count_out, cu_tokens, slots, positions, stream=None) -> int:
+    """Pages for the new tokens of a step, and each new token's slot and position."""
+    return int(_load().fd_page_tables(ctypes.byref(desc), _ptr(seqlens), _ptr(new_tokens), _ptr(free_pages),
+                                      _ptr(free_count), _ptr(block_table), _ptr(seqlens_out),
+                                      _ptr(free_count_out), _ptr(cu_tokens), _ptr(slots), _ptr(positions),
+                                      _stream(stream)))
+
+
+def fd_prompt_workspace_size(desc: FdPromptDesc) -> int:
+    return int(_load().fd_prompt_workspace_size(ctypes.byref(desc)))
+
+
+def fd_prompt(desc: FdPromptDesc, q, k, v, cu_q, cu_k, out, lse, workspace=None,
+              workspace_bytes: int | None = None, stream=None) -> int:
+    """Attention over whole prompts: packed sequences, causal or full."""
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    return int(_load().fd_prompt(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(out),
+                                 _ptr(lse), _ptr(workspace), int(wb), _stream(stream)))
+
+
 def fd_device_status(stream=None, clear: bool = True) -> int:
     return int(_load().fd_device_status(_stream(stream), 1 if clear else 0))
 
@@ -293,4 +385,87 @@ def make_desc(q, k_cache, v_cache, *, n_kv_heads: int | None = None, page_size: 
     d.q_dtype = _dtype_code(q.dtype)
     d.reserved = 0
     d.k_scale, d.v_scale = float(k_scale), float(v_scale)
+    return d
+
+
+def make_scales(k_scales, v_scales, *, block: int) -> FdKvScales:
+    """Block scales of an E4M3 cache: float32 [P, Hkv, page / block] (paged) or
+    [B, Hkv, ceil(T / block)] (contiguous), any strides.  The tensors are kept alive
+    by the returned object."""
+    import torch
+    s = FdKvScales()
+    for t in (k_scales, v_scales):
+        if t.dim() != 3 or t.dtype != torch.float32:
+            raise ValueError("scales must be float32 tensors of 3 dimensions")
+    s.k, s.v = k_scales.data_ptr(), v_scales.data_ptr()
+    s.k_stride_b, s.k_stride_h, s.k_stride_n = k_scales.stride()
+    s.v_stride_b, s.v_stride_h, s.v_stride_n = v_scales.stride()
+    s.block = int(block)
+    s.reserved = 0
+    s._keep = (k_scales, v_scales)
+    return s
+
+
+def make_store_desc(k, v, k_cache, v_cache, *, page_size: int = 0) -> FdStoreDesc:
+    """Descriptor for new rows k, v [n, Hkv, D] (16-bit, any strides with whole 16-byte
+    rows) into an E4M3 cache [P, Hkv, page, D] (paged) or [B, Hkv, T, D] (page_size 0)."""
+    d = FdStoreDesc()
+    d.n_tokens, d.n_kv_heads, d.head_dim = k.shape
+    if tuple(v.shape) != tuple(k.shape) or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same shape and type")
+    for c in (k_cache, v_cache):
+        if _dtype_code(c.dtype) != FD_E4M3 or c.dim() != 4 or c.shape[1] != d.n_kv_heads or c.shape[3] != d.head_dim:
+            raise ValueError("the caches must be float8_e4m3fn tensors [pages or sequences, Hkv, tokens, D]")
+        if page_size and c.shape[2] != page_size:
+            raise ValueError("a paged cache's third dimension is its page size")
+    if tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if k.stride(2) != 1 or v.stride(2) != 1 or k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        raise ValueError("the head dimension must be contiguous")
+    d.src_dtype = _dtype_code(k.dtype)
+    d.k_src_stride_t, d.k_src_stride_h = k.stride(0), k.stride(1)
+    d.v_src_stride_t, d.v_src_stride_h = v.stride(0), v.stride(1)
+    d.k_stride_b, d.k_stride_h, d.k_stride_t = k_cache.stride()[:3]
+    d.v_stride_b, d.v_stride_h, d.v_stride_t = v_cache.stride()[:3]
+    d.page_size = int(page_size)
+    d.kv_extent = k_cache.shape[0] if page_size else k_cache.shape[2]
+    d.batch = k_cache.shape[0]
+    return d
+
+
+def make_page_desc(block_table, free_pages, slots, *, page_size: int, n_pages: int) -> FdPageDesc:
+    """Descriptor for a table [B, max_pages_per_seq] (contiguous int32), the free stack and the slot map."""
+    if block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous [B, max_pages_per_seq] tensor")
+    d = FdPageDesc()
+    d.batch, d.max_pages_per_seq = block_table.shape
+    d.page_size, d.n_pages = int(page_size), int(n_pages)
+    d.n_free_max, d.n_slots = free_pages.numel(), slots.numel()
+    return d
+
+
+def make_prompt_desc(q, k, v, *, batch: int, causal: bool = True, max_q: int = 0, max_k: int = 0,
+                     n_splits: int = 0, out_dtype=None) -> FdPromptDesc:
+    """Descriptor for packed prompts q [total_q, Hq, D], k and v [total_k, Hkv, D]
+    (16-bit; any strides with a contiguous head dimension, so slices of one
+    projection's output too)."""
+    import torch
+    if not (q.dtype == k.dtype == v.dtype):
+        raise ValueError("q, k and v must have one type")
+    if k.shape != v.shape or q.shape[2] != k.shape[2]:
+        raise ValueError("q [total_q, Hq, D], k and v [total_k, Hkv, D]")
+    if q.stride(2) != 1 or k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("the head dimension must be contiguous")
+    d = FdPromptDesc()
+    d.batch = int(batch)
+    d.total_q, d.n_q_heads, d.head_dim = q.shape
+    d.total_k, d.n_kv_heads = k.shape[:2]
+    d.dtype = _dtype_code(q.dtype)
+    d.out_dtype = _dtype_code(out_dtype if out_dtype is not None else torch.float32)
+    d.q_stride_t, d.q_stride_h = q.stride(0), q.stride(1)
+    d.k_stride_t, d.k_stride_h = k.stride(0), k.stride(1)
+    d.v_stride_t, d.v_stride_h = v.stride(0), v.stride(1)
+    d.max_q, d.max_k = int(max_q), int(max_k)
+    d.causal, d.n_splits = int(bool(causal)), int(n_splits)
+    d.flags = d.reserved = 0
     return d

@@ -7,6 +7,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/fd.h"
@@ -38,6 +39,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // A stride in elements of `esize` bytes is usable by TMA: a multiple of 16 bytes.
 bool stride_ok(int64_t s, int esize = 2) {
     return s >= 0 && (s * esize) % 16 == 0 && s < (int64_t(1) << 38);
+}
+
+int log2_of(int32_t x) {   // of a power of two
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
 }
 
 bool is_fp8(const fd_desc* d) { return d->kv_dtype == FD_E4M3; }
@@ -182,7 +189,7 @@ fd_status make_map(CUtensorMap* map, const fd_desc* d, const void* base, int64_t
 fd_status split_impl(const fd_desc* d, int32_t S, const void* q, const void* k, const void* v,
                      const int32_t* seqlens, const int32_t* block_table, void* workspace,
                      size_t workspace_bytes, cudaStream_t stream, bool direct = false,
-                     void* out = nullptr, float* lse = nullptr) {
+                     void* out = nullptr, float* lse = nullptr, const fd_kv_scales* scales = nullptr) {
     // a direct one-split launch given no workspace never touches one
     const bool no_ws = direct && S == 1 && out != nullptr && workspace == nullptr;
     if (q == nullptr || k == nullptr || v == nullptr || seqlens == nullptr ||
@@ -244,10 +251,35 @@ fd_status split_impl(const fd_desc* d, int32_t S, const void* q, const void* k, 
     p.out_dtype = d->out_dtype == FD_F16 ? 0 : d->out_dtype == FD_BF16 ? 1 : 2;
     p.out = out;
     p.lse = lse;
+    p.scale_k = p.scale_v = nullptr;
+    if (scales != nullptr) {
+        p.scale_k = scales->k;
+        p.scale_v = scales->v;
+        p.scale_kb = scales->k_stride_b;
+        p.scale_kh = scales->k_stride_h;
+        p.scale_kn = scales->k_stride_n;
+        p.scale_vb = scales->v_stride_b;
+        p.scale_vh = scales->v_stride_h;
+        p.scale_vn = scales->v_stride_n;
+        p.scale_shift = log2_of(scales->block);
+    }
     const cudaError_t e = fdk::launch_split(tmK, tmV, p, q_type_of(d), is_fp8(d),
                                             (d->flags & FD_FLAG_CUDA_CORES) != 0, d->batch,
                                             d->n_kv_heads, stream);
     return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+// The block scales of an E4M3 cache with `page_size`-token pages (0: contiguous).
+fd_status check_scales(const fd_kv_scales* s, int32_t page_size) {
+    if (s == nullptr || s->k == nullptr || s->v == nullptr || s->reserved != 0) return FD_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(s->k) & 3u) != 0 || (reinterpret_cast<uintptr_t>(s->v) & 3u) != 0)
+        return FD_ERR_INVALID_ARG;
+    if (s->block < 1 || (s->block & (s->block - 1)) != 0) return FD_ERR_INVALID_ARG;
+    if (s->block > 1024) return FD_ERR_UNSUPPORTED;
+    if (page_size > 0 && s->block > page_size) return FD_ERR_INVALID_ARG;
+    for (const int64_t st : {s->k_stride_b, s->k_stride_h, s->k_stride_n, s->v_stride_b, s->v_stride_h, s->v_stride_n})
+        if (st < 0 || st >= (int64_t(1) << 38)) return FD_ERR_INVALID_ARG;
+    return FD_OK;
 }
 
 fd_status combine_impl(const fd_desc* d, int32_t S, const void* workspace, size_t workspace_bytes,
@@ -271,6 +303,54 @@ fd_status combine_impl(const fd_desc* d, int32_t S, const void* workspace, size_
     p.out_dtype = d->out_dtype == FD_F16 ? 0 : d->out_dtype == FD_BF16 ? 1 : 2;
     const cudaError_t e = fdk::launch_combine(p, stream);
     return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+// ---- prompts
+fd_status check_prompt(const fd_prompt_desc* d) {
+    if (d == nullptr || d->batch < 0 || d->n_q_heads < 1 || d->n_kv_heads < 1 || d->head_dim < 1 || d->total_q < 0 ||
+        d->total_k < 0 || d->max_q < 0 || d->max_k < 0)
+        return FD_ERR_INVALID_ARG;
+    if (d->n_q_heads % d->n_kv_heads != 0) return FD_ERR_INVALID_ARG;
+    if (d->flags != 0 || d->reserved != 0 || (d->causal != 0 && d->causal != 1)) return FD_ERR_INVALID_ARG;
+    if (d->dtype != FD_F16 && d->dtype != FD_BF16)
+        return d->dtype == FD_F32 || d->dtype == FD_E4M3 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (d->out_dtype != FD_F16 && d->out_dtype != FD_BF16 && d->out_dtype != FD_F32) return FD_ERR_INVALID_ARG;
+    if (d->head_dim != kHeadDim) return FD_ERR_UNSUPPORTED;
+    if (d->n_splits > FD_MAX_SPLITS || d->n_q_heads > 65535) return FD_ERR_UNSUPPORTED;
+    for (const int64_t s : {d->q_stride_t, d->q_stride_h, d->k_stride_t, d->k_stride_h, d->v_stride_t, d->v_stride_h})
+        if (!stride_ok(s)) return FD_ERR_INVALID_ARG;
+    if (d->q_stride_t < kHeadDim || d->k_stride_t < kHeadDim || d->v_stride_t < kHeadDim) return FD_ERR_INVALID_ARG;
+    return FD_OK;
+}
+
+bool pair_heads_of(const fd_prompt_desc* d) { return (d->n_q_heads / d->n_kv_heads) % 2 == 0; }
+
+// Query tiles per head unit: every sequence may end inside one.
+int64_t prompt_tiles(const fd_prompt_desc* d) {
+    return d->total_q / (pair_heads_of(d) ? 128 : 256) + d->batch;
+}
+
+int32_t prompt_splits(const fd_prompt_desc* d) {
+    if (d->n_splits >= 1) return d->n_splits;
+    return 1;
+}
+
+// 3-D map over packed rows: dims (head_dim, rows, heads), boxes of 64 dims x
+// 128 rows with 128-byte swizzle, zero fill outside.
+fd_status make_rows_map(CUtensorMap* map, bool bf16, const void* base, int64_t rows, int64_t heads, int64_t st, int64_t sh) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return FD_ERR_CUDA;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(heads), 1};
+    auto bs = [](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s * 2 : 16); };
+    cuuint64_t strides[3] = {bs(st), bs(sh), 16};
+    cuuint32_t box[4] = {64, 128, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                           const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FD_OK : FD_ERR_INVALID_ARG;
 }
 
 // ---- fixed workspace for fd_decode_static (callers that cannot allocate)
@@ -394,6 +474,25 @@ fd_status fd_decode(const fd_desc* desc, const void* q, const void* k_cache, con
     return combine_impl(desc, S, workspace, workspace_bytes, out, lse, s);
 }
 
+fd_status fd_decode_scaled(const fd_desc* desc, const fd_kv_scales* scales, const void* q,
+                           const void* k_cache, const void* v_cache, const int32_t* seqlens,
+                           const int32_t* block_table, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    fd_status st = check_desc(desc);
+    if (st != FD_OK) return st;
+    if (!is_fp8(desc)) return FD_ERR_INVALID_ARG;
+    st = check_scales(scales, desc->page_size);
+    if (st != FD_OK) return st;
+    if (out == nullptr) return FD_ERR_INVALID_ARG;
+    const int32_t S = splits_for(desc);
+    if (S < 1) return static_cast<fd_status>(S < 0 ? S : FD_ERR_INVALID_ARG);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = split_impl(desc, S, q, k_cache, v_cache, seqlens, block_table, workspace, workspace_bytes, s,
+                    S == 1, out, lse, scales);
+    if (st != FD_OK || S == 1) return st;
+    return combine_impl(desc, S, workspace, workspace_bytes, out, lse, s);
+}
+
 fd_status fd_decode_static(const fd_desc* desc, const void* q, const void* k_cache,
                            const void* v_cache, const int32_t* seqlens, const int32_t* block_table,
                            void* out, float* lse, void* stream) {
@@ -420,6 +519,168 @@ fd_status fd_decode_static(const fd_desc* desc, const void* q, const void* k_cac
     return combine_impl(desc, S, ws, FD_STATIC_WORKSPACE_BYTES, out, lse, s);
 }
 
+fd_status fd_cache_store(const fd_store_desc* d, const fd_kv_scales* scales, const void* k, const void* v,
+                         const int64_t* slots, void* k_cache, void* v_cache, void* stream) {
+    if (d == nullptr || d->n_tokens < 0 || d->n_kv_heads < 1 || d->head_dim < 1) return FD_ERR_INVALID_ARG;
+    if (d->src_dtype != FD_F16 && d->src_dtype != FD_BF16)
+        return d->src_dtype == FD_F32 || d->src_dtype == FD_E4M3 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (d->head_dim != kHeadDim) return FD_ERR_UNSUPPORTED;
+    if (d->page_size < 0) return FD_ERR_INVALID_ARG;
+    if (d->page_size > 0) {
+        if ((d->page_size & (d->page_size - 1)) != 0 || d->page_size > (1 << 20)) return FD_ERR_INVALID_ARG;
+        if (d->page_size < 8) return FD_ERR_UNSUPPORTED;
+    } else if (d->batch < 1) {
+        return FD_ERR_INVALID_ARG;
+    }
+    if (d->kv_extent < 1 || d->kv_extent > INT32_MAX) return FD_ERR_INVALID_ARG;
+    if (!stride_ok(d->k_src_stride_t) || !stride_ok(d->k_src_stride_h) || !stride_ok(d->v_src_stride_t) ||
+        !stride_ok(d->v_src_stride_h))
+        return FD_ERR_INVALID_ARG;
+    if (!stride_ok(d->k_stride_b, 1) || !stride_ok(d->k_stride_h, 1) || !stride_ok(d->k_stride_t, 1) ||
+        !stride_ok(d->v_stride_b, 1) || !stride_ok(d->v_stride_h, 1) || !stride_ok(d->v_stride_t, 1))
+        return FD_ERR_INVALID_ARG;
+    if (d->k_stride_t < kHeadDim || d->v_stride_t < kHeadDim) return FD_ERR_INVALID_ARG;
+    const fd_status st = check_scales(scales, d->page_size);
+    if (st != FD_OK) return st;
+    if (d->n_kv_heads > 65535) return FD_ERR_UNSUPPORTED;
+    if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr || v_cache == nullptr)
+        return FD_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+        return FD_ERR_INVALID_ARG;
+    if (d->n_tokens == 0) return FD_OK;
+    fdk::StoreParams p;
+    p.side[0] = {k, static_cast<uint8_t*>(k_cache), scales->k, d->k_src_stride_t, d->k_src_stride_h,
+                 d->k_stride_b, d->k_stride_h, d->k_stride_t, scales->k_stride_b, scales->k_stride_h, scales->k_stride_n};
+    p.side[1] = {v, static_cast<uint8_t*>(v_cache), scales->v, d->v_src_stride_t, d->v_src_stride_h,
+                 d->v_stride_b, d->v_stride_h, d->v_stride_t, scales->v_stride_b, scales->v_stride_h, scales->v_stride_n};
+    p.slots = slots;
+    const bool paged = d->page_size > 0;
+    p.row_tokens = paged ? d->page_size : static_cast<int32_t>(d->kv_extent);
+    p.n_slots = (paged ? d->kv_extent : static_cast<int64_t>(d->batch)) * p.row_tokens;
+    p.block = scales->block;
+    p.n_tokens = d->n_tokens;
+    p.n_kv_heads = d->n_kv_heads;
+    return fdk::launch_store(p, d->src_dtype == FD_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK
+                                                                                                      : FD_ERR_CUDA;
+}
+
+fd_status fd_page_tables(const fd_page_desc* d, const int32_t* seqlens, const int32_t* new_tokens,
+                         const int32_t* free_pages, const int32_t* free_count, int32_t* block_table,
+                         int32_t* seqlens_out, int32_t* free_count_out, int32_t* cu_tokens, int64_t* slots,
+                         int32_t* positions, void* stream) {
+    if (d == nullptr || d->batch < 0 || d->page_size < 1 || (d->page_size & (d->page_size - 1)) != 0 ||
+        d->page_size > (1 << 20) || d->max_pages_per_seq < 1 || d->n_pages < 1 || d->n_free_max < 0 || d->n_slots < 0)
+        return FD_ERR_INVALID_ARG;
+    if (d->page_size < 8 || d->batch > FD_MAX_TABLE_BATCH) return FD_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(d->max_pages_per_seq) * d->page_size > INT32_MAX) return FD_ERR_INVALID_ARG;
+    if (free_count == nullptr || free_count_out == nullptr || (d->n_free_max > 0 && free_pages == nullptr) ||
+        (d->n_slots > 0 && slots == nullptr))
+        return FD_ERR_INVALID_ARG;
+    if (d->batch > 0 && (seqlens == nullptr || new_tokens == nullptr || block_table == nullptr || seqlens_out == nullptr))
+        return FD_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return FD_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(seqlens), static_cast<const void*>(new_tokens),
+                          static_cast<const void*>(free_pages), static_cast<const void*>(free_count),
+                          static_cast<const void*>(block_table), static_cast<const void*>(seqlens_out),
+                          static_cast<const void*>(free_count_out), static_cast<const void*>(cu_tokens),
+                          static_cast<const void*>(positions)})
+        if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return FD_ERR_INVALID_ARG;
+    fdk::PageParams p;
+    p.seqlens = seqlens;
+    p.new_tokens = new_tokens;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.block_table = block_table;
+    p.seqlens_out = seqlens_out;
+    p.free_count_out = free_count_out;
+    p.cu_tokens = cu_tokens;
+    p.slots = slots;
+    p.positions = positions;
+    p.batch = d->batch;
+    p.page_size = d->page_size;
+    p.page_shift = log2_of(d->page_size);
+    p.max_pages = d->max_pages_per_seq;
+    p.n_pages = d->n_pages;
+    p.n_free_max = d->n_free_max;
+    p.n_slots = d->n_slots;
+    return fdk::launch_page_tables(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+size_t fd_prompt_workspace_size(const fd_prompt_desc* desc) {
+    if (check_prompt(desc) != FD_OK) return 0;
+    const int32_t S = prompt_splits(desc);
+    if (S <= 1) return 0;
+    return ws_layout(static_cast<int64_t>(desc->total_q) * desc->n_q_heads, S).total;
+}
+
+fd_status fd_prompt(const fd_prompt_desc* d, const void* q, const void* k, const void* v, const int32_t* cu_q,
+                    const int32_t* cu_k, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+    fd_status st = check_prompt(d);
+    if (st != FD_OK) return st;
+    if (d->batch == 0 || d->total_q == 0) return FD_OK;
+    if (q == nullptr || out == nullptr || cu_q == nullptr || cu_k == nullptr ||
+        (d->total_k > 0 && (k == nullptr || v == nullptr)))
+        return FD_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return FD_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(cu_q) & 3u) != 0 || (reinterpret_cast<uintptr_t>(cu_k) & 3u) != 0)
+        return FD_ERR_INVALID_ARG;
+    const int32_t S = prompt_splits(d);
+    if (S < 1) return static_cast<fd_status>(S < 0 ? S : FD_ERR_INVALID_ARG);
+    const WsLayout w = ws_layout(static_cast<int64_t>(d->total_q) * d->n_q_heads, S);
+    if (S > 1 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0 ||
+                  workspace_bytes < w.total))
+        return FD_ERR_WORKSPACE;
+    fdk::PromptParams p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_st = d->q_stride_t;
+    p.q_sh = d->q_stride_h;
+    p.k_st = d->k_stride_t;
+    p.k_sh = d->k_stride_h;
+    p.v_st = d->v_stride_t;
+    p.v_sh = d->v_stride_h;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.out = out;
+    p.lse = lse;
+    char* ws = static_cast<char*>(workspace);
+    p.ws_u = S > 1 ? reinterpret_cast<float*>(ws + w.off_u) : nullptr;
+    p.ws_m = S > 1 ? reinterpret_cast<float*>(ws + w.off_m) : nullptr;
+    p.ws_l = S > 1 ? reinterpret_cast<float*>(ws + w.off_l) : nullptr;
+    p.batch = d->batch;
+    p.n_q_heads = d->n_q_heads;
+    p.group = d->n_q_heads / d->n_kv_heads;
+    p.total_q = d->total_q;
+    p.total_k = d->total_k;
+    p.causal = d->causal;
+    p.n_splits = S;
+    p.pair_heads = pair_heads_of(d) ? 1 : 0;
+    p.head_units = p.pair_heads ? d->n_q_heads / 2 : d->n_q_heads;
+    p.out_dtype = d->out_dtype == FD_F16 ? 0 : d->out_dtype == FD_BF16 ? 1 : 2;
+    p.out_vec = aligned16(out) ? 1 : 0;
+    p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHeadDim)));
+    const int64_t tiles = prompt_tiles(d);
+    if (tiles * p.head_units * S > INT32_MAX) return FD_ERR_UNSUPPORTED;
+    const bool bf16 = d->dtype == FD_BF16;
+    CUtensorMap tmQ, tmK, tmV;
+    st = make_rows_map(&tmQ, bf16, q, d->total_q, d->n_q_heads, d->q_stride_t, d->q_stride_h);
+    if (st != FD_OK) return st;
+    if (d->total_k > 0) {
+        st = make_rows_map(&tmK, bf16, k, d->total_k, d->n_kv_heads, d->k_stride_t, d->k_stride_h);
+        if (st != FD_OK) return st;
+        st = make_rows_map(&tmV, bf16, v, d->total_k, d->n_kv_heads, d->v_stride_t, d->v_stride_h);
+        if (st != FD_OK) return st;
+    } else {
+        tmK = tmV = tmQ;             // no key is ever read
+    }
+    return fdk::launch_prompt(tmQ, tmK, tmV, p, bf16, tiles, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FD_OK
+               : FD_ERR_CUDA;
+}
+
 int32_t fd_plan_desc(const fd_desc* desc, const int32_t* seqlens_host, int32_t num_sms) {
     fd_status st = check_desc(desc);
     if (st != FD_OK) return st;
@@ -438,6 +699,9 @@ fd_status fd_decode_status(void* stream) { return fd_device_status(stream, 1); }
 fd_status fd_device_status(void* stream, int32_t clear) {
     unsigned v = 0;
     if (fdk::read_status(&v, static_cast<cudaStream_t>(stream), clear != 0) != cudaSuccess)
+        return FD_ERR_CUDA;
+    if (fdk::status_tables(&v, clear != 0) != cudaSuccess || fdk::status_store(&v, clear != 0) != cudaSuccess ||
+        fdk::status_prompt(&v, clear != 0) != cudaSuccess)
         return FD_ERR_CUDA;
     if (v & fdk::kStatusTimeoutBit) return FD_ERR_DEVICE_TIMEOUT;
     if (v != 0) return FD_ERR_DEVICE_BOUNDS;

@@ -61,6 +61,12 @@ struct SplitParams {
     int32_t out_dtype;              // 0 f16, 1 bf16, 2 f32
     void* out;                      // [rows][D]
     float* lse;                     // [rows] or null
+    // block scales of an fp8 cache (null: none): token t of page / sequence b,
+    // KV head g has scale_k[b scale_kb + g scale_kh + (t >> scale_shift) scale_kn]
+    const float* scale_k;
+    const float* scale_v;
+    int64_t scale_kb, scale_kh, scale_kn, scale_vb, scale_vh, scale_vn;
+    int32_t scale_shift;
 };
 
 struct CombineParams {
@@ -128,6 +134,80 @@ int32_t plan_launch(int64_t batch, int64_t n_kv_heads, int cols, bool fp8, bool 
 // (the fixed workspace's address, kernel attributes) is keyed on it.
 unsigned long long current_context_id();
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
+
+// ---- page tables, store into a block-scaled cache, prompt attention
+
+struct PageParams {
+    const int32_t* seqlens;
+    const int32_t* new_tokens;
+    const int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* block_table;
+    int32_t* seqlens_out;
+    int32_t* free_count_out;
+    int32_t* cu_tokens;             // or null
+    int64_t* slots;
+    int32_t* positions;             // or null
+    int32_t batch, page_size, page_shift, max_pages, n_pages, n_free_max, n_slots;
+};
+cudaError_t launch_page_tables(const PageParams& p, cudaStream_t stream);
+
+struct StoreSide {                  // K or V; strides in elements
+    const void* src;
+    uint8_t* dst;
+    float* scale;
+    int64_t src_t, src_h, dst_b, dst_h, dst_t, scale_b, scale_h, scale_n;
+};
+struct StoreParams {
+    StoreSide side[2];
+    const int64_t* slots;
+    int64_t n_slots;                // places in the cache
+    int32_t row_tokens;             // tokens per page, or per sequence of a contiguous cache
+    int32_t block;                  // tokens per scale
+    int32_t n_tokens, n_kv_heads;
+};
+cudaError_t launch_store(const StoreParams& p, bool bf16, cudaStream_t stream);
+
+struct PromptParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;   // elements
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    void* out;
+    float* lse;                     // or null
+    float* ws_u;                    // n_splits > 1: [rows][n_splits][D], row = t n_q_heads + h
+    float* ws_m;                    // base-2 units
+    float* ws_l;
+    int32_t batch, n_q_heads, group, total_q, total_k, causal, n_splits;
+    int32_t pair_heads;             // a CTA's two query tiles: two heads (1) or 256 positions (0)
+    int32_t head_units;             // n_q_heads / 2 or n_q_heads
+    int32_t out_dtype;              // 0 f16, 1 bf16, 2 f32
+    int32_t out_vec;                // out is 16-byte aligned
+    float scale_log2;               // log2(e) / sqrt(D)
+};
+// tiles: query tiles (of 128 positions, or 256) that the sequences can have at most.
+cudaError_t launch_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                          const PromptParams& p, bool bf16, int64_t tiles, cudaStream_t stream);
+cudaError_t status_prompt(unsigned* value, bool clear);
+
+// Each file that raises status bits owns a word; fd_device_status joins them.
+// Called with the stream already synchronised.
+#ifdef __CUDACC__
+inline cudaError_t read_status_word(unsigned& symbol, unsigned* value, bool clear) {
+    unsigned v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, symbol, sizeof(unsigned));
+    if (e == cudaSuccess && clear && v != 0) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(symbol, &zero, sizeof(unsigned));
+    }
+    *value |= v;
+    return e;
+}
+#endif
+cudaError_t status_tables(unsigned* value, bool clear);
+cudaError_t status_store(unsigned* value, bool clear);
 
 // Device status word helpers (fd_split.cu owns the symbol).
 cudaError_t read_status(unsigned* value, cudaStream_t stream, bool clear);

@@ -178,9 +178,11 @@ template <int KIND>
 struct Geo {
     static constexpr bool kUmma = KIND == 31 || KIND == 32;    // tcgen05 consumers, see below
     static constexpr bool kF8 = KIND >= 20 && !kUmma;
-    static constexpr int kWarps = KIND == 21 ? kConsumerWarpsF8 : kUmma ? 8 : kConsumerWarps;
+    static constexpr bool kScaled = KIND == 23 || KIND == 24;  // 21, 22 with block scales
+    static constexpr bool kNarrow = KIND == 21 || KIND == 23;  // fp8, up to 8 columns
+    static constexpr int kWarps = kNarrow ? kConsumerWarpsF8 : kUmma ? 8 : kConsumerWarps;
     static constexpr int kSub = kUmma ? 64 : 16 * kWarps;      // tokens per stage
-    static constexpr int kRing = KIND == 21 ? 4 : KIND == 22 ? 6 : kUmma ? 6 : kStages;
+    static constexpr int kRing = kNarrow ? 4 : kF8 ? 6 : kUmma ? 6 : kStages;
     static constexpr int kTile = kSub * 128;                   // one box of 128-byte rows
     static constexpr int kStageBytes = (kF8 ? 2 : 4) * kTile;
     // tcgen05: consecutive stages land side by side in pairs, so that one MMA
@@ -204,7 +206,9 @@ struct Geo {
     static constexpr bool kOwnMap = kF8 || kUmma;
     static_assert(!kUmma || kSub == fdk::kSub, "the tcgen05 variant streams the 16-bit stages");
     static constexpr int kOffFlag = (kOwnMap ? kOffBars + 128 : fdk::kOffFlag);
-    static constexpr int kSmem = (kOwnMap ? kOffFlag + 16 : kSmemUsed) + 1024;   // + alignment slack
+    static constexpr int kOffScale = kOffFlag + 16;            // block scales: [kRing][K, V][kSub] f32
+    static constexpr int kScaleBytes = kScaled ? kRing * 2 * kSub * 4 : 0;
+    static constexpr int kSmem = (kOwnMap ? kOffFlag + 16 + kScaleBytes : kSmemUsed) + 1024;   // + alignment slack
     // a CTA that serves two splits at once (see fd_split_kernel) gives each this much
     static constexpr int kSmemHalf = (kSmem - 1024 + 1023) / 1024 * 1024;
     // + one TMA producer warp (+ one MMA-issuing warp for tcgen05)
@@ -328,6 +332,95 @@ __device__ __forceinline__ void produce(const SplitCtx& c, const CUtensorMap* tm
     if (lane == 0) {
         for (int i = max(first, issued - kStages); i < issued; ++i)
             wait_or_flag(c.full_bar(i % kStages), (i / kStages) & 1);
+    }
+}
+
+// Producer warp of an fp8 cache with block scales: the stages of produce(), and
+// beside each its tokens' K and V scales as floats in shared memory (two plain
+// loads per token, looked up through the block table for a paged cache).  A
+// stage's bytes are requested as soon as its slot is free; its one arrival on
+// the full barrier comes later, when its scales are written, which were
+// requested a stage before.  Tokens past the split's end get scale 0.
+template <int KIND>
+__device__ __forceinline__ void produce_scaled(const SplitCtx& c, const CUtensorMap* tmK,
+                                               const CUtensorMap* tmV, int lane) {
+    using Gm = Geo<KIND>;
+    constexpr int kRing = Gm::kRing;
+    constexpr int kSub = Gm::kSub;
+    constexpr int kPer = kSub / 32;                                      // tokens per lane and stage
+    const SplitParams& p = *c.p;
+    const uint64_t policy = p.col_blocks > 1 ? policy_evict_normal() : policy_evict_first();
+    const bool paged = p.page_size != 0;
+    const int rows = paged ? min(kPagedBoxRows, p.page_size) : kSub;   // tokens per box
+    const int nbox = kSub / rows;
+    const int32_t* table = p.block_table + static_cast<size_t>(c.b) * p.max_pages;   // (paged)
+    auto page_at = [&](int t) -> int {             // page of token t; -1 outside the split or the pool
+        if (t >= c.tok1) return -1;
+        const int pg = __ldg(table + (t >> p.page_shift));
+        if (pg >= 0 && pg < p.n_pages) return pg;
+        raise_status(kStatusPageBit);
+        return -1;
+    };
+    const int first = p.drop_first_stage ? 1 : 0;   // test hook: stage 0 is never requested
+    auto issue = [&](int i) {
+        if (i < first) return;
+        const int tok = c.tok0 + i * kSub;
+        const uint32_t dst = smem_u32(c.smem) + Gm::stage_off(i % kRing);
+        const uint32_t bar = c.full_bar(i % kRing);
+        const int outer = paged ? (lane < nbox ? page_at(tok + lane * rows) : -1) : c.b;
+        if (lane == 0) mbar_expect_tx(bar, Gm::kStageBytes);
+        __syncwarp();
+        if (lane < (paged ? nbox : 1)) {
+            const int row = paged ? (tok + lane * rows) & (p.page_size - 1) : tok;
+            const uint32_t off = static_cast<uint32_t>(lane * rows * 128);
+            tma_load_4d_hint(dst + off, tmK, bar, 0, row, c.kvh, outer, policy);
+            tma_load_4d_hint(dst + Gm::kTile + off, tmV, bar, 0, row, c.kvh, outer, policy);
+        }
+    };
+    auto load_scales = [&](int i, float (&ks)[kPer], float (&vs)[kPer]) {
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int t = c.tok0 + i * kSub + 32 * x + lane;
+            const int lead = i >= c.n_sub || t >= c.tok1 ? -1 : paged ? page_at(t) : c.b;
+            const int64_t n = (paged ? t & (p.page_size - 1) : t) >> p.scale_shift;
+            ks[x] = vs[x] = 0.f;
+            if (lead >= 0) {
+                ks[x] = __ldg(p.scale_k + lead * p.scale_kb + c.kvh * p.scale_kh + n * p.scale_kn);
+                vs[x] = __ldg(p.scale_v + lead * p.scale_vb + c.kvh * p.scale_vh + n * p.scale_vn);
+            }
+        }
+    };
+    float ks[kPer], vs[kPer];
+    load_scales(0, ks, vs);
+    int issued = 0, arrived = 0;
+    for (; issued < min(kRing, c.n_sub); ++issued) issue(issued);
+#pragma unroll 1
+    for (int i = 0; i < c.n_sub; ++i) {
+        float kn[kPer], vn[kPer];
+        load_scales(i + 1, kn, vn);
+        float* dst = reinterpret_cast<float*>(c.smem + Gm::kOffScale) + (i % kRing) * 2 * kSub;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            dst[32 * x + lane] = ks[x];
+            dst[kSub + 32 * x + lane] = vs[x];
+            ks[x] = kn[x];
+            vs[x] = vn[x];
+        }
+        __syncwarp();
+        if (lane == 0 && i >= first) mbar_arrive(c.full_bar(i % kRing));
+        arrived = i + 1;
+        if (i >= 1 && issued < c.n_sub) {          // the slot of stage i - 1 next
+            const bool ok = wait_or_flag(c.empty_bar((i - 1) % kRing), ((i - 1) / kRing) & 1);
+            if (!__all_sync(kFull, ok)) *c.abort_flag = 1;
+            if (*c.abort_flag) break;
+            issue(issued++);
+        }
+    }
+    // Drain as in produce(); a stage given up before its arrival gets it here.
+    if (lane == 0) {
+        for (int i = max(first, arrived); i < issued; ++i) mbar_arrive(c.full_bar(i % kRing));
+        for (int i = max(first, issued - kRing); i < issued; ++i)
+            wait_or_flag(c.full_bar(i % kRing), (i / kRing) & 1);
     }
 }
 
@@ -668,6 +761,76 @@ __device__ __forceinline__ void rescale_acc(float (&acc)[8][NB][4], const float 
         }
 }
 
+// softmax_tiles for one tile of a cache with block scales: token gid (gid + 8)
+// has K scale ks[0] (ks[1]) and V scale 2^lv[0] (2^lv[1]).  The V scale enters the
+// weights of PV, p' = 2^(t + lv - mv), with a running max mv of its own: p' stays
+// in f16's range however the scales differ from block to block (and a zero
+// scale, lv = -inf, gives 0), while l keeps the weights 2^(t - m).  The
+// accumulators follow mv; `al` is their factor.
+template <int NB>
+__device__ __forceinline__ bool softmax_scaled(const float (&s)[NB][4], const float (&csc)[NB][2],
+                                               const float (&ks)[2], const float (&lv)[2], const int (&vis)[NB][2],
+                                               int nvalid, int tok, int row0, int row1, bool masked,
+                                               float (&m)[NB][2], float (&mv)[NB][2], float (&l)[NB][2],
+                                               float (&al)[NB][2], uint32_t (&bh)[NB][2], uint32_t (&bl)[NB][2]) {
+    bool rescale = false;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        float t[4], w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = s[j][e] * (csc[j][e & 1] * ks[e >> 1]);
+        if (masked) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int lim = min(nvalid, vis[j][e] - tok);
+                if (row0 >= lim) t[e] = -INFINITY;
+                if (row1 >= lim) t[e + 2] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = t[e] + lv[e >> 1];
+        bool up = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            up |= fmaxf(t[e], t[e + 2]) > m[j][e] + kLazyMax || fmaxf(w[e], w[e + 2]) > mv[j][e] + kLazyMax;
+        const bool move = __any_sync(kFull, up);
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float mn = m[j][e], mvn = mv[j][e];
+            if (move) {   // warp-uniform
+                float x = fmaxf(t[e], t[e + 2]), y = fmaxf(w[e], w[e + 2]);
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) {
+                    x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+                    y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
+                }
+                mn = fmaxf(mn, x);
+                mvn = fmaxf(mvn, y);
+            }
+            const float mu = mn == -INFINITY ? 0.f : mn, mvu = mvn == -INFINITY ? 0.f : mvn;
+            const float a = move ? fast_exp2(m[j][e] - mu) : 1.f;
+            al[j][e] = move ? fast_exp2(mv[j][e] - mvu) : 1.f;
+            l[j][e] = fmaf(a, l[j][e], fast_exp2(t[e] - mu) + fast_exp2(t[e + 2] - mu));
+            pr[e] = fast_exp2(w[e] - mvu);
+            pr[e + 2] = fast_exp2(w[e + 2] - mvu);
+            m[j][e] = mn;
+            mv[j][e] = mvn;
+            rescale |= al[j][e] != 1.f;
+        }
+        float k0, k1, k2, k3, d0, d1, d2, d3;
+        const uint32_t hi01 = Mma<__half>::pack(pr[0], pr[1], k0, k1);
+        const uint32_t hi23 = Mma<__half>::pack(pr[2], pr[3], k2, k3);
+        const uint32_t lo01 = Mma<__half>::pack(pr[0] - k0, pr[1] - k1, d0, d1);
+        const uint32_t lo23 = Mma<__half>::pack(pr[2] - k2, pr[3] - k3, d2, d3);
+        bh[j][0] = movmatrix_trans(hi01);
+        bh[j][1] = movmatrix_trans(hi23);
+        bl[j][0] = movmatrix_trans(lo01);
+        bl[j][1] = movmatrix_trans(lo23);
+    }
+    return __any_sync(kFull, rescale);
+}
+
 // Keys visible to the lane's C columns: column n is query position n / G and
 // sees the first L - q_len + 1 + n / G keys.
 template <int NB>
@@ -881,7 +1044,7 @@ __device__ __forceinline__ void unpack4(const uint4& r, uint32_t* w) {
 template <typename T, int KIND>
 __device__ __forceinline__ bool consume_f8(const SplitCtx& c, int cw, int lane) {
     using Gm = Geo<KIND>;
-    constexpr int NB = KIND == 21 ? 1 : 2;
+    constexpr int NB = Gm::kNarrow ? 1 : 2;
     constexpr int kSub = Gm::kSub;
     constexpr int kRing = Gm::kRing;
     const SplitParams& p = *c.p;
@@ -943,10 +1106,11 @@ __device__ __forceinline__ bool consume_f8(const SplitCtx& c, int cw, int lane) 
     visible_keys<NB>(c, tig, vis);
 
     float m[NB][2], l[NB][2];
+    [[maybe_unused]] float mv[NB][2];            // block scales: the reference of acc (of l: m)
     float acc[8][NB][4];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        m[j][0] = m[j][1] = -INFINITY;
+        m[j][0] = m[j][1] = mv[j][0] = mv[j][1] = -INFINITY;
         l[j][0] = l[j][1] = 0.f;
 #pragma unroll
         for (int mb = 0; mb < 8; ++mb)
@@ -986,6 +1150,14 @@ __device__ __forceinline__ bool consume_f8(const SplitCtx& c, int cw, int lane) 
         unpack4(*reinterpret_cast<const uint4*>(sb + k_off1 + 8 * 128), kw + 12);
 #pragma unroll
         for (int x = 0; x < 4; ++x) unpack4(*reinterpret_cast<const uint4*>(sb + v_off[x]), vw[x]);
+        [[maybe_unused]] float ksc[2], lv[2];
+        if constexpr (Gm::kScaled) {
+            const float* sc = reinterpret_cast<const float*>(c.smem + Gm::kOffScale) + st * 2 * kSub + r0 + gid;
+            ksc[0] = sc[0];
+            ksc[1] = sc[8];
+            lv[0] = __log2f(sc[kSub]);
+            lv[1] = __log2f(sc[kSub + 8]);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(c.empty_bar(st));   // the stage is in registers
         const bool partial = nvalid < kSub;            // the split's last stage
@@ -1024,11 +1196,16 @@ __device__ __forceinline__ bool consume_f8(const SplitCtx& c, int cw, int lane) 
 
         float al[NB][2];
         uint32_t bh[1][NB][2], bl[1][NB][2];
-        const int nv[1] = {nvalid}, tk[1] = {tok};
-        if (softmax_tiles<__half, NB, 1>(s, csc, vis, nv, tk, r0 + gid, r0 + gid + 8,
-                                         partial || tok + kSub > c.L - p.q_len + 1, m, l, al, bh,
-                                         bl))
-            rescale_acc<NB>(acc, al);
+        const bool masked = partial || tok + kSub > c.L - p.q_len + 1;
+        if constexpr (Gm::kScaled) {
+            if (softmax_scaled<NB>(s[0], csc, ksc, lv, vis, nvalid, tok, r0 + gid, r0 + gid + 8, masked, m, mv, l, al,
+                                   bh[0], bl[0]))
+                rescale_acc<NB>(acc, al);
+        } else {
+            const int nv[1] = {nvalid}, tk[1] = {tok};
+            if (softmax_tiles<__half, NB, 1>(s, csc, vis, nv, tk, r0 + gid, r0 + gid + 8, masked, m, l, al, bh, bl))
+                rescale_acc<NB>(acc, al);
+        }
 
         // ---- O^T += V^T . P^T (permuted dims)
 #pragma unroll
@@ -1046,6 +1223,15 @@ __device__ __forceinline__ bool consume_f8(const SplitCtx& c, int cw, int lane) 
         }
     }
 
+    if constexpr (Gm::kScaled) {   // acc to the reference of l, as the merge takes both
+        float f[NB][2];
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                f[j][e] = m[j][e] == -INFINITY || mv[j][e] == -INFINITY ? 0.f : fast_exp2(mv[j][e] - m[j][e]);
+        rescale_acc<NB>(acc, f);
+    }
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
@@ -1083,7 +1269,7 @@ __device__ __forceinline__ bool consume_f8(const SplitCtx& c, int cw, int lane) 
 template <typename T, int KIND>
 struct Consumer;
 // KIND 1, 2: tensor cores with 8 or 16 columns; 21, 22: the same on an fp8
-// cache; KIND 10 + G: CUDA cores, group G
+// cache; 23, 24: those with block scales; KIND 10 + G: CUDA cores, group G
 template <typename T> struct Consumer<T, 1> {
     static __device__ bool run(const SplitCtx& c, int w, int l) { return consume_tc<T, 1>(c, w, l); }
 };
@@ -1095,6 +1281,12 @@ template <typename T> struct Consumer<T, 21> {
 };
 template <typename T> struct Consumer<T, 22> {
     static __device__ bool run(const SplitCtx& c, int w, int l) { return consume_f8<T, 22>(c, w, l); }
+};
+template <typename T> struct Consumer<T, 23> {
+    static __device__ bool run(const SplitCtx& c, int w, int l) { return consume_f8<T, 23>(c, w, l); }
+};
+template <typename T> struct Consumer<T, 24> {
+    static __device__ bool run(const SplitCtx& c, int w, int l) { return consume_f8<T, 24>(c, w, l); }
 };
 template <typename T> struct Consumer<T, 11> {
     static __device__ bool run(const SplitCtx& c, int w, int l) { return consume_simt<T, 1>(c, w, l); }
@@ -1259,7 +1451,8 @@ __global__ void __launch_bounds__(Geo<KIND>::kThreads * HALVES, HALVES == 1 ? 2 
     if (idle) return;
 
     if (warp == kWarps) {
-        produce<KIND>(c, &tmK, &tmV, lane);
+        if constexpr (Gm::kScaled) produce_scaled<KIND>(c, &tmK, &tmV, lane);
+        else produce<KIND>(c, &tmK, &tmV, lane);
         return;
     }
 
@@ -2098,7 +2291,7 @@ static cudaError_t launch_split_t(const CUtensorMap& tmK, const CUtensorMap& tmV
     // wave holds those CTAs (a CTA of two takes a whole SM, and an odd split
     // count leaves a half idle per (sequence, KV head); beyond one wave the
     // CTAs of one, two to an SM, quantise better)
-    if constexpr (KIND == 21) {
+    if constexpr (Gm::kNarrow) {
         const int sms = fd_num_sms(-1);
         const int64_t heads = static_cast<int64_t>(n_kv_heads) * batch;
         if (blocks * heads > sms && ((blocks + 1) / 2) * heads <= sms) {
@@ -2130,6 +2323,9 @@ static cudaError_t launch_split_dt(const CUtensorMap& tmK, const CUtensorMap& tm
     if (use_umma(fp8, cuda_cores, p.cols))
         return p.cols <= 64 ? launch_split_umma<T, 32>(tmK, tmV, p, batch, n_kv_heads, stream)
                             : launch_split_umma<T, 31>(tmK, tmV, p, batch, n_kv_heads, stream);
+    if (fp8 && p.scale_k != nullptr)
+        return p.cols <= 8 ? launch_split_t<T, 23>(tmK, tmV, p, batch, n_kv_heads, stream)
+                           : launch_split_t<T, 24>(tmK, tmV, p, batch, n_kv_heads, stream);
     if (fp8)
         return p.cols <= 8 ? launch_split_t<T, 21>(tmK, tmV, p, batch, n_kv_heads, stream)
                            : launch_split_t<T, 22>(tmK, tmV, p, batch, n_kv_heads, stream);
