@@ -71,7 +71,8 @@ enum Bar : int {
     kBarP = kBarS + 2,          // [2 tiles][2 halves] P written (and O rescaled), one arrival per warp
     kBarO = kBarP + 4,          // [2] PV done (MMA commit)
     kBarV = kBarO + 2,          // [4] a masked tile's V is guarded, by its number mod 4
-    kBarDrain = kBarV + 4,      // every MMA done
+    kBarG = kBarV + 4,          // [4] a masked tile's V landed and waits for the guard
+    kBarDrain = kBarG + 4,      // every MMA done
     kBars
 };
 static_assert(kBars * 8 <= 256, "barriers");
@@ -414,6 +415,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int j = j0; ok && j < n; ++j) {
                 const int i = 2 * (j - j0) + 1;
                 bool guarded = j < w.guard;      // nothing to wait for
+                if (!guarded) {
+                    need(i);
+                    mbar_arrive(bar(kBarG + ((j - w.guard) & 3)));
+                }
                 for (int t = 0; ok && t < 2; ++t) {
                     if (j >= w.n[t]) continue;
                     need(i);
@@ -446,7 +451,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // ---- guard of V in the tiles where some row's limit falls
         for (int j = max(j0, w.guard); j < n; ++j) {
             const int i = 2 * (j - j0) + 1, s = i % kSlots;
-            const bool ok = wait_bar(bar(kBarFull + s), (i / kSlots) & 1, abort_flag);
+            // (the MMA thread says when: a warp that waits for a phase of the ring's
+            // barrier long before it begins would take an older phase for it)
+            const uint32_t x4 = (j - w.guard) & 3, par = ((j - w.guard) >> 2) & 1;
+            const bool ok = wait_bar(bar(kBarG + x4), par, abort_flag) &&
+                            wait_bar(bar(kBarFull + s), (i / kSlots) & 1, abort_flag);
             if (!__all_sync(kFullMask, ok)) break;
             uint8_t* v = smem + kOffRing + s * kSlotBytes;
             const int rows = min(kTile, w.nk - j * kTile);   // of this sequence
@@ -460,7 +469,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (bad) *special = 1;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarV + ((j - w.guard) & 3)));
+            if (lane == 0) mbar_arrive(bar(kBarV + x4));
         }
         __syncwarp();
     } else {
