@@ -558,7 +558,9 @@ fd_status fd_cache_store(const fd_store_desc* d, const fd_kv_scales* scales, con
     const bool paged = d->page_size > 0;
     p.row_tokens = paged ? d->page_size : static_cast<int32_t>(d->kv_extent);
     p.n_slots = (paged ? d->kv_extent : static_cast<int64_t>(d->batch)) * p.row_tokens;
+    p.row_shift = paged ? log2_of(d->page_size) : -1;
     p.block = scales->block;
+    p.block_shift = log2_of(scales->block);
     p.n_tokens = d->n_tokens;
     p.n_kv_heads = d->n_kv_heads;
     return fdk::launch_store(p, d->src_dtype == FD_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK

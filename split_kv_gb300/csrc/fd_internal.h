@@ -163,7 +163,8 @@ struct StoreParams {
     const int64_t* slots;
     int64_t n_slots;                // places in the cache
     int32_t row_tokens;             // tokens per page, or per sequence of a contiguous cache
-    int32_t block;                  // tokens per scale
+    int32_t row_shift;              // log2(row_tokens) of pages; -1 for a contiguous cache
+    int32_t block, block_shift;     // tokens per scale
     int32_t n_tokens, n_kv_heads;
 };
 cudaError_t launch_store(const StoreParams& p, bool bf16, cudaStream_t stream);
