@@ -84,6 +84,28 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     return false;
 }
 
+// A value that every lane has, known to the compiler as warp-uniform.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(kFullMask, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFullMask, x, 0); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// wait_bar by a whole warp, which leaves it together.
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(kFullMask, wait_bar(bar, parity, abort_flag));
+}
+
+// umma_idesc_f16 of 128 x 128 as a constant
+constexpr uint32_t umma_idesc(bool bf16, bool b_mn_major) {
+    return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
+}
+
 // What one CTA does: two query tiles and the key tiles [j0, j1) of one sequence.
 struct Work {
     int b;                      // -1: nothing
@@ -304,7 +326,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t bar0 = smem_u32(smem + kOffBar);
     auto bar = [&](int i) { return bar0 + 8u * i; };
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 256);
@@ -377,76 +399,134 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
     } else if (warp == 9) {
-        // ---- MMA issue
-        if (lane == 0 && n > j0) {
+        // ---- MMA issue: the whole warp walks the tiles, one elected lane issues.
+        // Everything the MMAs take is warp-uniform for the compiler (the
+        // shuffles), so that descriptors stay in uniform registers: from inside
+        // a one-lane branch an MMA cost its thread 113 cycles, with 64 the tensor
+        // cores' own time.
+        const int m_n0 = uniform(n0), m_n1 = uniform(n1), m_j0 = uniform(j0), m_guard = uniform(w.guard);
+        const int m_n = max(m_n0, m_n1);
+        if (m_n > m_j0) {
             constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-            const uint32_t id_s = umma_idesc_f16(128, 128, kBf16, false);
-            const uint32_t id_o = umma_idesc_f16(128, 128, kBf16, true);
-            const uint64_t dq = umma_desc_sw128(smem_u32(smem), 16, 1024);
-            const uint64_t dk = umma_desc_sw128(smem_u32(smem + kOffRing), 16, 1024);
-            const uint64_t dv = umma_desc_sw128(smem_u32(smem + kOffRing), kHalf, 1024);
+            constexpr uint32_t id_s = umma_idesc(kBf16, false), id_o = umma_idesc(kBf16, true);
+            const uint32_t sm = uniform(smem_u32(smem)), tm = uniform(tmem), b0 = uniform(bar0);
+            const uint64_t dq = umma_desc_sw128(sm, 16, 1024);
+            const uint64_t dk = umma_desc_sw128(sm + kOffRing, 16, 1024);
+            const uint64_t dv = umma_desc_sw128(sm + kOffRing, kHalf, 1024);
+            const bool leader = elect_one();
             bool ok = true;
-            int full_upto = 0;                   // ring entries known to have landed
-            auto need = [&](int i) {             // ring entry i
-                while (ok && full_upto <= i) {
-                    ok = wait_bar(bar(kBarFull + full_upto % kSlots), (full_upto / kSlots) & 1, abort_flag);
-                    ++full_upto;
+            auto wait = [&](int i, uint32_t parity) {
+                if (ok) ok = wait_bar_warp(b0 + 8u * i, parity, abort_flag);
+            };
+            int slot = 0;                        // ring slot of the entry at hand, and the parity of its use
+            uint32_t use = 0;
+            auto next_slot = [&]() {
+                if (++slot == kSlots) {
+                    slot = 0;
+                    use ^= 1u;
                 }
             };
-            auto last_user = [&](int t, int j) { return t == 1 || j >= n1; };
-            auto issue_s = [&](int t, int j) {
-                const int i = 2 * (j - j0);
-                if (j == j0) ok = ok && wait_bar(bar(kBarQ + t), 0, abort_flag);
-                need(i);
+            // S of tile t from the K at `slot`
+            auto issue_s = [&](auto tile, bool last) {
+                constexpr int t = decltype(tile)::value;
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t a = dq + static_cast<uint32_t>(t) * (kSlotBytes >> 4);
-                const uint64_t b = dk + static_cast<uint32_t>(i % kSlots) * (kSlotBytes >> 4);
+                const uint64_t a = dq + static_cast<uint32_t>(t * (kSlotBytes >> 4));
+                const uint64_t b = dk + static_cast<uint32_t>(slot) * (kSlotBytes >> 4);
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4;
-                    umma_f16(tmem + 128u * t, a + off, b + off, id_s, kk > 0);
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4;
+                        umma_f16(tm + 128u * t, a + off, b + off, id_s, kk > 0);
+                    }
+                    umma_commit(b0 + 8u * (kBarS + t));
+                    if (last) umma_commit(b0 + 8u * (kBarEmpty + slot));
                 }
-                umma_commit(bar(kBarS + t));
-                if (last_user(t, j)) umma_commit(bar(kBarEmpty + i % kSlots));
+                __syncwarp();
             };
-            if (run0) issue_s(0, j0);
-            if (ok && run1) issue_s(1, j0);
-            for (int j = j0; ok && j < n; ++j) {
-                const int i = 2 * (j - j0) + 1;
-                bool guarded = j < w.guard;      // nothing to wait for
-                if (!guarded) {
-                    need(i);
-                    mbar_arrive(bar(kBarG + ((j - w.guard) & 3)));
-                }
-                for (int t = 0; ok && t < 2; ++t) {
-                    if (j >= w.n[t]) continue;
-                    need(i);
-                    if (!guarded) {
-                        ok = ok && wait_bar(bar(kBarV + ((j - w.guard) & 3)), ((j - w.guard) >> 2) & 1, abort_flag);
-                        guarded = true;
-                    }
-                    const uint64_t b = dv + static_cast<uint32_t>(i % kSlots) * (kSlotBytes >> 4);
-                    const uint32_t o = tmem + 256u + 128u * t, a = tmem + 128u * t;
+            // half h of PV of tile t from the V at `slot`
+            auto issue_pv = [&](auto tile, int h, bool first) {
+                constexpr int t = decltype(tile)::value;
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t b = dv + static_cast<uint32_t>(slot) * (kSlotBytes >> 4) + static_cast<uint32_t>(h * 4 * (2048 >> 4));
+                if (leader) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && wait_bar(bar(kBarP + 2 * t + h), (j - j0) & 1, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                            umma_f16_ta(o, a + 8u * kk, b + ((kk * 2048u) >> 4), id_o, j > j0 || kk > 0);
-                    }
-                    if (!ok) break;
-                    umma_commit(bar(kBarO + t));
-                    if (last_user(t, j)) umma_commit(bar(kBarEmpty + i % kSlots));
-                    if (j + 1 < w.n[t]) issue_s(t, j + 1);
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ta(tm + 256u + 128u * t, tm + 128u * t + 32u * h + 8u * kk,
+                                    b + static_cast<uint32_t>(kk * (2048 >> 4)), id_o, !(first && kk == 0));
                 }
+                __syncwarp();
+            };
+            using Tile0 = std::integral_constant<int, 0>;
+            using Tile1 = std::integral_constant<int, 1>;
+            const bool act0 = m_n0 > m_j0, act1 = m_n1 > m_j0;
+            if (act0) wait(kBarQ, 0);
+            wait(kBarFull, 0);
+            if (act0) issue_s(Tile0{}, !act1);
+            if (act1) {
+                wait(kBarQ + 1, 0);
+                issue_s(Tile1{}, true);
             }
-            umma_commit(bar(kBarDrain));
-            wait_bar(bar(kBarDrain), 0, abort_flag);
+            next_slot();
+            uint32_t turn = 0;                   // parity of the tile's number
+            for (int j = m_j0; ok && j < m_n; ++j, turn ^= 1u) {
+                // `slot` is V of tile j; the next one is K of tile j + 1
+                const int v_slot = slot;
+                const uint32_t v_use = use;
+                const bool more0 = j + 1 < m_n0, more1 = j + 1 < m_n1;
+                wait(kBarFull + v_slot, v_use);
+                if (j >= m_guard) {              // some row's limit falls in this tile
+                    const int g = (j - m_guard) & 3;
+                    if (leader) mbar_arrive(b0 + 8u * (kBarG + g));
+                    __syncwarp();
+                    wait(kBarV + g, ((j - m_guard) >> 2) & 1);
+                }
+                next_slot();
+                const int k_slot = slot;
+                const uint32_t k_use = use;
+                if (j < m_n0) {
+                    slot = v_slot;
+                    wait(kBarP, turn);
+                    issue_pv(Tile0{}, 0, j == m_j0);
+                    wait(kBarP + 1, turn);
+                    issue_pv(Tile0{}, 1, false);
+                    if (ok && leader) {
+                        umma_commit(b0 + 8u * kBarO);
+                        if (j >= m_n1) umma_commit(b0 + 8u * (kBarEmpty + v_slot));
+                    }
+                    __syncwarp();
+                    slot = k_slot;
+                    if (more0) {
+                        wait(kBarFull + k_slot, k_use);
+                        issue_s(Tile0{}, !more1);
+                    }
+                }
+                if (j < m_n1) {
+                    slot = v_slot;
+                    wait(kBarP + 2, turn);
+                    issue_pv(Tile1{}, 0, j == m_j0);
+                    wait(kBarP + 3, turn);
+                    issue_pv(Tile1{}, 1, false);
+                    if (ok && leader) {
+                        umma_commit(b0 + 8u * (kBarO + 1));
+                        umma_commit(b0 + 8u * (kBarEmpty + v_slot));
+                    }
+                    __syncwarp();
+                    slot = k_slot;
+                    if (more1) {
+                        if (!more0) wait(kBarFull + k_slot, k_use);
+                        issue_s(Tile1{}, true);
+                    }
+                }
+                slot = k_slot;
+                use = k_use;
+                next_slot();
+            }
+            if (leader) umma_commit(b0 + 8u * kBarDrain);
+            __syncwarp();
+            wait_bar_warp(b0 + 8u * kBarDrain, 0, abort_flag);
         }
-        __syncwarp();
     } else if (warp == 10) {
         // ---- guard of V in the tiles where some row's limit falls
         for (int j = max(j0, w.guard); j < n; ++j) {
