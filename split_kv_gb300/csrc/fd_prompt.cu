@@ -9,11 +9,11 @@
 // p stays below 2^8 and O is rescaled only then); any reference gives the same
 // result up to rounding.
 //
-// One CTA takes two query tiles of 128 rows and walks the key tiles of 128 they
-// see.  The two tiles are the same positions of two heads of one group where
-// the group is even (both then see the same keys, and a causal pair wastes
-// half a tile on the diagonal, not one and a half), else 256 positions of one
-// head.  Per key tile and query tile:
+// An item is two query tiles of 128 rows and the key tiles of 128 they see.  The
+// two tiles are the same positions of two heads of one group where the group is
+// even (both then see the same keys, and a causal pair wastes half a tile on the
+// diagonal, not one and a half), else 256 positions of one head.  Per key tile
+// and query tile:
 //   S[128 x 128] = Q K^T      8 MMAs of 16 dims, operands in shared memory
 //   O[128 x 128] += P V       8 MMAs of 16 keys, P from tensor memory
 // Warps 0-3 and 4-7 are the softmax of tile 0 and 1, a thread per row: it reads
@@ -21,15 +21,22 @@
 // unrounded weights) over it, in two halves so that PV starts on the first
 // while the second is computed.  Warp 8 streams K and V tiles with TMA through
 // a ring of five 32 KB slots, warp 9 issues the MMAs: while one tile's softmax
-// runs, the tensor cores work on the other tile's PV and next S.  Warp 10
-// guards the masked tiles (below).
+// runs, the tensor cores work on the other tile's PV and next S.  Warp 10 guards
+// the masked tiles (below), warp 11 hands out the items.
 // Tensor memory (512 columns): S/P of tile 0, 1 at 0, 128; O at 256, 384.
+//
+// Persistent: one CTA per SM takes items in turn.  The roles run ahead of each
+// other: the next item's Q and K are loaded and its first S is computed while
+// the softmax warps still write out the item before (only its first PV waits
+// until they have read O).  Items come largest first (by the key tiles they
+// see, over all sequences; found by bisection over the sequences' lengths) and
+// are dealt out back and forth, which leaves the CTAs about equal sums.
 //
 // Masked places: scores past a row's limit are replaced by -inf before they
 // are used, so what K holds there does not matter.  P is 0 there, but 0 * NaN
 // is NaN, so in the (last) tiles where some row's limit falls, warp 10 zeroes
 // the V rows past the sequence's end and looks for infinities and NaN in the
-// others; only if it finds one are the CTA's rows computed again by a plain
+// others; only if it finds one are the item's rows computed again by a plain
 // loop over the keys each row sees.
 //
 // Bound by the tensor cores when sequences are long: 4 * 128 flops per visible
@@ -58,24 +65,35 @@ constexpr int kSlotBytes = kTile * 256; // [128 x 64 dims] low half, high half
 constexpr int kHalf = kSlotBytes / 2;
 constexpr int kOffRing = 2 * kSlotBytes;
 constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-constexpr int kSmem = kOffBar + 512 + 1024;
-constexpr int kPromptThreads = 11 * 32;
+constexpr int kOffWork = kOffBar + 384; // [kWorks] Work, 64 bytes each
+constexpr int kWorks = 4;
+constexpr int kOffMisc = kOffWork + kWorks * 64;    // tensor memory address, abort flag, [kWorks] special flags
+constexpr int kOffLens = kOffMisc + 32; // cu_q and cu_k of up to kSorted sequences
+constexpr int kSorted = 128;            // batches up to this are handed out largest first
+constexpr int kSmem = kOffLens + 2 * (kSorted + 1) * 4 + 1024;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr int kPromptThreads = 12 * 32;
 constexpr float kLazy = 8.f;
 
-// mbarriers, 8 bytes each from kOffBar
+// mbarriers, 8 bytes each from kOffBar.  Every role keeps its own counts of the
+// uses of a barrier across items; a wait's parity is that of the use.
 enum Bar : int {
     kBarQ = 0,                  // [2] a tile's Q landed
-    kBarFull = 2,               // [kSlots]
+    kBarQE = 2,                 // [2] the last S of an item's tile done: Q's place is free (MMA commit)
+    kBarFull = 4,               // [kSlots]
     kBarEmpty = kBarFull + kSlots,
     kBarS = kBarEmpty + kSlots, // [2] S written (MMA commit)
     kBarP = kBarS + 2,          // [2 tiles][2 halves] P written (and O rescaled), one arrival per warp
     kBarO = kBarP + 4,          // [2] PV done (MMA commit)
-    kBarV = kBarO + 2,          // [4] a masked tile's V is guarded, by its number mod 4
-    kBarG = kBarV + 4,          // [4] a masked tile's V landed and waits for the guard
-    kBarDrain = kBarG + 4,      // every MMA done
+    kBarOF = kBarO + 2,         // [2] an item's O read out, one arrival per warp
+    kBarG = kBarOF + 2,         // [4] a masked tile's V landed and waits for the guard, by its number mod 4
+    kBarV = kBarG + 4,          // [4] it is guarded
+    kBarWF = kBarV + 4,         // [kWorks] an item is handed out
+    kBarWE = kBarWF + kWorks,   // [kWorks] every role is done with it: producer, MMA, guard, 8 softmax warps
+    kBarDrain = kBarWE + kWorks,// every MMA done
     kBars
 };
-static_assert(kBars * 8 <= 256, "barriers");
+static_assert(kBars * 8 <= 384, "barriers");
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     if (mbar_wait(bar, parity)) return true;
@@ -106,67 +124,37 @@ constexpr uint32_t umma_idesc(bool bf16, bool b_mn_major) {
     return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
 }
 
-// What one CTA does: two query tiles and the key tiles [j0, j1) of one sequence.
+// One item: two query tiles and the key tiles [j0, j1) of one sequence.
 struct Work {
-    int b;                      // -1: nothing
+    int b;                      // -1: no more items
     int q0, k0, nq, nk;         // the sequence's rows
     int head[2], pos[2];        // of the two query tiles
-    int n[2];                   // key tiles each sees, from 0 (0: inactive)
+    int n[2];                   // key tiles each sees, from 0 (<= j0: inactive)
     int j0, j1;                 // key tiles of this split
     int guard;                  // first key tile where some row's limit falls
     int split;
 };
+static_assert(sizeof(Work) <= 64, "work");
 
 __device__ __forceinline__ int seen_by(const PromptParams& p, int nq, int nk, int i) {
     return p.causal ? min(max(nk - nq + 1 + i, 0), nk) : nk;
 }
 
-// The work of block `block`, found by one warp.  Blocks are (query tile, head
-// unit, split), splits fastest; a sequence's tiles come last first, since the
-// last ones see the most keys.
-__device__ __forceinline__ void find_work(const PromptParams& p, int64_t block, int lane, Work& w, bool report) {
-    const int split = static_cast<int>(block % p.n_splits);
-    const int64_t rest = block / p.n_splits;
-    const int unit = static_cast<int>(rest % p.head_units);
-    int tile = static_cast<int>(rest / p.head_units);
-    w.b = -1;
-    const int span = p.pair_heads ? kTile : 2 * kTile;   // positions per CTA
-    for (int base = 0; base < p.batch; base += 32) {
-        const int b = base + lane;
-        int a = 0, e = 0, ka = 0, ke = 0;
-        if (b < p.batch) {
-            a = p.cu_q[b];
-            e = p.cu_q[b + 1];
-            ka = p.cu_k[b];
-            ke = p.cu_k[b + 1];
-        }
-        const bool ok = a >= 0 && e >= a && e <= p.total_q && ka >= 0 && ke >= ka && ke <= p.total_k;
-        if (!ok && report) atomicOr(&g_status, kStatusSeqlenBit);
-        const int tiles = ok ? (e - a + span - 1) / span : 0;
-        int upto = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFullMask, upto, o);
-            if (lane >= o) upto += y;
-        }
-        const unsigned hit = __ballot_sync(kFullMask, tile < upto);
-        const int all = __shfl_sync(kFullMask, upto, 31);
-        if (hit != 0 && w.b < 0) {
-            const int src = __ffs(hit) - 1;
-            const int mine = tile - (upto - tiles);      // this lane's view of the tile's number
-            w.b = base + src;
-            w.q0 = __shfl_sync(kFullMask, a, src);
-            w.nq = __shfl_sync(kFullMask, e, src) - w.q0;
-            w.k0 = __shfl_sync(kFullMask, ka, src);
-            w.nk = __shfl_sync(kFullMask, ke, src) - w.k0;
-            const int from_end = __shfl_sync(kFullMask, mine, src);
-            tile = __shfl_sync(kFullMask, tiles, src) - 1 - from_end;
-            if (!report) break;
-        } else if (w.b < 0) {
-            tile -= all;
-        }
-    }
-    if (w.b < 0) return;
+__device__ __forceinline__ int span_of(const PromptParams& p) { return p.pair_heads ? kTile : 2 * kTile; }
+
+// Whether a sequence's offsets hold; its numbers of queries and keys.
+__device__ __forceinline__ bool read_seq(const PromptParams& p, const int* cq, const int* ck, int& q0, int& nq, int& k0,
+                                         int& nk) {
+    q0 = cq[0];
+    k0 = ck[0];
+    nq = cq[1] - q0;
+    nk = ck[1] - k0;
+    return q0 >= 0 && cq[1] >= q0 && cq[1] <= p.total_q && k0 >= 0 && ck[1] >= k0 && ck[1] <= p.total_k;
+}
+
+// The item (tile `tile` of the sequence in w, head unit, split): the rest of w.
+__device__ __forceinline__ void fill_work(const PromptParams& p, int tile, int unit, int split, Work& w) {
+    const int span = span_of(p);
     w.split = split;
     int most = 0;
 #pragma unroll
@@ -185,6 +173,122 @@ __device__ __forceinline__ void find_work(const PromptParams& p, int64_t block, 
     w.n[1] = min(w.n[1], w.j1);
     w.guard = max(w.j0, seen_by(p, w.nq, w.nk, w.pos[0]) / kTile);
 }
+
+// Hands out items by their rank, one warp.  Ranks count (query tile, head unit,
+// split), splits fastest.  Up to kSorted sequences (sorted): tiles in order of
+// the key tiles they see, most first; beyond: as the sequences come, each
+// one's last tile first (ranks have to ascend).
+struct Dealer {
+    const int* cq;              // sorted: shared memory copies
+    const int* ck;
+    bool sorted;
+    int top;                    // sorted: the most key tiles any sequence has
+    int base, before;           // else: the chunk of 32 sequences looked at, tiles before it
+
+    // tiles of a sequence that see at least `need` key tiles
+    __device__ __forceinline__ int tiles_seeing(const PromptParams& p, int nq, int nk, int need) const {
+        const int span = span_of(p), tiles = (nq + span - 1) / span;
+        if (need <= 0) return tiles;
+        const int x = (need - 1) * kTile + 1;           // keys
+        if (nk < x) return 0;
+        if (!p.causal) return tiles;
+        const int rows = x - nk + nq;                    // the first so many rows see fewer
+        return tiles - (rows <= 0 ? 0 : (rows + span - 1) / span - 1);
+    }
+    __device__ __forceinline__ int all_seeing(const PromptParams& p, int need, int lane) const {
+        int sum = 0;
+        for (int c = 0; c < p.batch; c += 32) {
+            int q0, nq, k0, nk;
+            if (c + lane < p.batch && read_seq(p, cq + c + lane, ck + c + lane, q0, nq, k0, nk))
+                sum += tiles_seeing(p, nq, nk, need);
+        }
+        return __reduce_add_sync(kFullMask, sum);
+    }
+    __device__ __forceinline__ void start(const PromptParams& p, int* shared_lens, int lane, bool report) {
+        sorted = p.batch <= kSorted;
+        base = before = top = 0;
+        cq = p.cu_q;
+        ck = p.cu_k;
+        if (!sorted) return;
+        int* sq = shared_lens;
+        int* sk = shared_lens + kSorted + 1;
+        for (int i = lane; i <= p.batch; i += 32) {
+            sq[i] = p.cu_q[i];
+            sk[i] = p.cu_k[i];
+        }
+        __syncwarp();
+        cq = sq;
+        ck = sk;
+        int most = 0;
+        bool bad = false;
+        for (int c = lane; c < p.batch; c += 32) {
+            int q0, nq, k0, nk;
+            if (read_seq(p, cq + c, ck + c, q0, nq, k0, nk)) most = max(most, (nk + kTile - 1) / kTile);
+            else bad = true;
+        }
+        top = __reduce_max_sync(kFullMask, most);
+        if (report && bad) atomicOr(&g_status, kStatusSeqlenBit);
+    }
+    // (every lane gets the item; b = -1 past the last one)
+    __device__ __forceinline__ void item(const PromptParams& p, int64_t rank, int lane, Work& w) {
+        const int split = static_cast<int>(rank % p.n_splits);
+        const int64_t rest = rank / p.n_splits;
+        const int unit = static_cast<int>(rest % p.head_units);
+        const int64_t at = rest / p.head_units;          // the tile's rank
+        w.b = -1;
+        int need = 0;                                    // key tiles of the tile with that rank
+        int64_t idx = at;
+        if (sorted) {
+            if (at >= all_seeing(p, 0, lane)) return;
+            int hi = top + 1;
+            while (hi - need > 1) {
+                const int mid = (need + hi) >> 1;
+                if (all_seeing(p, mid, lane) > at) need = mid;
+                else hi = mid;
+            }
+            idx = at - all_seeing(p, need + 1, lane);    // among those that see exactly `need`
+            before = 0;
+            base = 0;
+        }
+        for (; base < p.batch; base += 32) {
+            int q0 = 0, nq = 0, k0 = 0, nk = 0, mine = 0, tile0 = 0;
+            if (base + lane < p.batch && read_seq(p, cq + base + lane, ck + base + lane, q0, nq, k0, nk)) {
+                const int all = tiles_seeing(p, nq, nk, 0);
+                const int from = sorted ? tiles_seeing(p, nq, nk, need) : all;
+                mine = sorted ? from - tiles_seeing(p, nq, nk, need + 1) : all;
+                tile0 = all - from;                      // the first of these tiles
+            }
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFullMask, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const unsigned hit = __ballot_sync(kFullMask, idx - before < upto);
+            if (hit != 0) {
+                const int src = __ffs(hit) - 1;
+                const int i = static_cast<int>(idx - before) - (upto - mine);
+                w.b = base + src;
+                w.q0 = __shfl_sync(kFullMask, q0, src);
+                w.nq = __shfl_sync(kFullMask, nq, src);
+                w.k0 = __shfl_sync(kFullMask, k0, src);
+                w.nk = __shfl_sync(kFullMask, nk, src);
+                const int tile = __shfl_sync(kFullMask, sorted ? tile0 + i : mine - 1 - i, src);
+                fill_work(p, tile, unit, split, w);
+                return;
+            }
+            before += __shfl_sync(kFullMask, upto, 31);
+        }
+    }
+    // unsorted: offsets of every sequence
+    __device__ __forceinline__ void report_all(const PromptParams& p, int lane) const {
+        if (sorted) return;
+        for (int c = lane; c < p.batch; c += 32) {
+            int q0, nq, k0, nk;
+            if (!read_seq(p, p.cu_q + c, p.cu_k + c, q0, nq, k0, nk)) atomicOr(&g_status, kStatusSeqlenBit);
+        }
+    }
+};
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -310,6 +414,40 @@ __device__ __noinline__ void plain_row(const PromptParams& p, const Work& w, int
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Four running maxima over 64 scores (set by the first call).
+template <bool FIRST>
+__device__ __forceinline__ void row_max(const uint32_t (&s)[64], float (&mx)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = __uint_as_float(s[e]), b = __uint_as_float(s[e + 4]);
+        mx[e] = FIRST ? fmaxf(a, b) : max3(mx[e], a, b);
+    }
+#pragma unroll
+    for (int c = 8; c < 64; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4]));
+}
+
+// The weights 2^(s sc + b) of 64 scores as 16-bit pairs, and their 32-bit sums;
+// two at a time where the arithmetic has a form for it.
+template <typename T>
+__device__ __forceinline__ void weights(const uint32_t (&s)[64], float sc, float b, uint32_t (&pw)[32], float2 (&sum)[2]) {
+    const float2 sc2 = make_float2(sc, sc), b2 = make_float2(b, b);
+#pragma unroll
+    for (int c = 0; c < 64; c += 2) {
+        const float2 t = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, b2);
+        const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+        sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
+        pw[c / 2] = pack2<T>(e.x, e.y);
+    }
+}
+
 // Any infinity or NaN among the eight 16-bit values of a piece: an exponent of
 // all ones carries into the sign bit when one more is added.
 template <typename T>
@@ -329,87 +467,93 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t bar0 = smem_u32(smem + kOffBar);
     auto bar = [&](int i) { return bar0 + 8u * i; };
-    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + 256);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 260);
-    volatile int* special = reinterpret_cast<volatile int*>(smem + kOffBar + 264);
-    Work* shared_work = reinterpret_cast<Work*>(smem + kOffBar + 272);
-    static_assert(272 + sizeof(Work) <= 512, "work");
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+    volatile int* special = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);   // [kWorks]
+    auto work_at = [&](int k) { return reinterpret_cast<Work*>(smem + kOffWork + 64 * (k % kWorks)); };
 
     if (threadIdx.x == 256) {
-        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i >= kBarP && i < kBarP + 4 ? 4 : 1);
+        for (int i = 0; i < kBars; ++i)
+            mbar_init(bar(i), (i >= kBarP && i < kBarP + 4) || (i >= kBarOF && i < kBarOF + 2) ? 4
+                              : i >= kBarWE && i < kBarWE + kWorks                             ? 11
+                                                                                               : 1);
         *abort_flag = 0;
-        *special = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
+    if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
     grid_dependency_trigger();
     grid_dependency_wait();
-    if (warp == 0) {
-        Work w;
-        find_work(p, blockIdx.x, lane, w, blockIdx.x == 0);
-        if (lane == 0) *shared_work = w;
-    }
-    __syncthreads();
-    const Work w = *shared_work;
-    if (w.b < 0) return;
-    const int n0 = w.n[0], n1 = w.n[1], j0 = w.j0;
-    const int n = max(n0, n1);
-    const bool run0 = n0 > j0, run1 = n1 > j0;
-
-    if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*const_cast<uint32_t*>(tmem_slot));
 
-    if (warp == 8) {
-        // ---- producer: Q of both tiles, then K and V of each key tile
-        if (lane == 0 && n > j0) {
-            const int g = w.head[0] / p.group;
-            auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t b, int row, int head) {
-                mbar_arrive_expect_tx(b, kSlotBytes);
-                tma_load_4d(smem_u32(dst), map, b, 0, row, head, 0);
-                tma_load_4d(smem_u32(dst + kHalf), map, b, 64, row, head, 0);
-            };
-            if (run0) load(smem, &tmQ, bar(kBarQ), w.q0 + w.pos[0], w.head[0]);
-            int i = 0;
-            bool ok = true;
-            auto tile = [&](const CUtensorMap* map, int j) {
-                const int s = i % kSlots;
-                if (i >= kSlots) ok = ok && wait_bar(bar(kBarEmpty + s), (i / kSlots - 1) & 1, abort_flag);
-                if (!ok || *abort_flag) {
-                    ok = false;
-                    return;
+    // The softmax warps take registers from the others: 256 * 208 + 128 * 88 =
+    // 384 * 168, what the launch has.
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) {
+            // ---- producer: Q of both tiles, then K and V of each key tile
+            if (lane == 0) {
+                auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t b, int row, int head) {
+                    mbar_arrive_expect_tx(b, kSlotBytes);
+                    tma_load_4d(smem_u32(dst), map, b, 0, row, head, 0);
+                    tma_load_4d(smem_u32(dst + kHalf), map, b, 64, row, head, 0);
+                };
+                int i = 0, nq[2] = {0, 0};           // ring entries, Q tiles loaded
+                bool ok = true;
+                auto tile = [&](const CUtensorMap* map, int row, int head) {
+                    const int s = i % kSlots;
+                    if (i >= kSlots) ok = ok && wait_bar(bar(kBarEmpty + s), (i / kSlots - 1) & 1, abort_flag);
+                    if (!ok || *abort_flag) {
+                        ok = false;
+                        return;
+                    }
+                    load(smem + kOffRing + s * kSlotBytes, map, bar(kBarFull + s), row, head);
+                    ++i;
+                };
+                auto load_q = [&](const Work& w, int t) {
+                    if (!ok || w.n[t] <= w.j0) return;
+                    if (nq[t] > 0) ok = wait_bar(bar(kBarQE + t), (nq[t] - 1) & 1, abort_flag);
+                    if (!ok) return;
+                    load(smem + t * kSlotBytes, &tmQ, bar(kBarQ + t), w.q0 + w.pos[t], w.head[t]);
+                    ++nq[t];
+                };
+                for (int k = 0; ok; ++k) {
+                    ok = wait_bar(bar(kBarWF + k % kWorks), (k / kWorks) & 1, abort_flag);
+                    if (!ok) break;
+                    const Work w = *work_at(k);
+                    mbar_arrive(bar(kBarWE + k % kWorks));
+                    if (w.b < 0) break;
+                    const int n = max(w.n[0], w.n[1]), g = w.head[0] / p.group;
+                    if (n <= w.j0) continue;
+                    // the first K before the Qs: its slot is free sooner than theirs
+                    tile(&tmK, w.k0 + w.j0 * kTile, g);
+                    load_q(w, 0);
+                    load_q(w, 1);
+                    for (int j = w.j0; ok && j < n; ++j) {
+                        tile(&tmV, w.k0 + j * kTile, g);
+                        if (ok && j + 1 < n) tile(&tmK, w.k0 + (j + 1) * kTile, g);
+                    }
                 }
-                load(smem + kOffRing + s * kSlotBytes, map, bar(kBarFull + s), w.k0 + j * kTile, g);
-                ++i;
-            };
-            tile(&tmK, j0);
-            if (run1) load(smem + kSlotBytes, &tmQ, bar(kBarQ + 1), w.q0 + w.pos[1], w.head[1]);
-            for (int j = j0; ok && j < n; ++j) {
-                tile(&tmV, j);
-                if (ok && j + 1 < n) tile(&tmK, j + 1);
+                // nothing may be in flight towards this CTA when it exits
+                for (int t = 0; t < 2; ++t)
+                    if (nq[t] > 0) wait_bar(bar(kBarQ + t), (nq[t] - 1) & 1, abort_flag);
+                for (int x = max(0, i - kSlots); x < i; ++x) wait_bar(bar(kBarFull + x % kSlots), (x / kSlots) & 1, abort_flag);
             }
-            // nothing may be in flight towards this CTA when it exits
-            if (run0) wait_bar(bar(kBarQ), 0, abort_flag);
-            if (run1) wait_bar(bar(kBarQ + 1), 0, abort_flag);
-            for (int x = max(0, i - kSlots); x < i; ++x) wait_bar(bar(kBarFull + x % kSlots), (x / kSlots) & 1, abort_flag);
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        // ---- MMA issue: the whole warp walks the tiles, one elected lane issues.
-        // Everything the MMAs take is warp-uniform for the compiler (the
-        // shuffles), so that descriptors stay in uniform registers: from inside
-        // a one-lane branch an MMA cost its thread 113 cycles, with 64 the tensor
-        // cores' own time.
-        const int m_n0 = uniform(n0), m_n1 = uniform(n1), m_j0 = uniform(j0), m_guard = uniform(w.guard);
-        const int m_n = max(m_n0, m_n1);
-        if (m_n > m_j0) {
+            __syncwarp();
+        } else if (warp == 9) {
+            // ---- MMA issue: the whole warp walks the tiles, one elected lane issues.
+            // Everything the MMAs take is warp-uniform for the compiler (the
+            // shuffles), so that descriptors stay in uniform registers: from inside
+            // a one-lane branch an MMA cost its thread 113 cycles, with 64 the tensor
+            // cores' own time.
             constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
             constexpr uint32_t id_s = umma_idesc(kBf16, false), id_o = umma_idesc(kBf16, true);
-            const uint32_t sm = uniform(smem_u32(smem)), tm = uniform(tmem), b0 = uniform(bar0);
+            const uint32_t sm = uniform(smem_u32(smem)), b0 = uniform(bar0);
             const uint64_t dq = umma_desc_sw128(sm, 16, 1024);
             const uint64_t dk = umma_desc_sw128(sm + kOffRing, 16, 1024);
             const uint64_t dv = umma_desc_sw128(sm + kOffRing, kHalf, 1024);
@@ -418,7 +562,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             auto wait = [&](int i, uint32_t parity) {
                 if (ok) ok = wait_bar_warp(b0 + 8u * i, parity, abort_flag);
             };
-            int slot = 0;                        // ring slot of the entry at hand, and the parity of its use
+            auto commit = [&](int i) { umma_commit(b0 + 8u * i); };
+            int slot = 0;                            // ring slot of the entry at hand, and the parity of its use
             uint32_t use = 0;
             auto next_slot = [&]() {
                 if (++slot == kSlots) {
@@ -426,233 +571,272 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     use ^= 1u;
                 }
             };
-            // S of tile t from the K at `slot`
-            auto issue_s = [&](auto tile, bool last) {
+            uint32_t turn0 = 0, turn1 = 0;           // parities: P of tile 0, 1,
+            int items0 = 0, items1 = 0;              // items in which tile 0, 1 ran
+            int guarded = 0;
+            // S of tile t from the K at `ks`; `last`: its last reader; `end`: the item's last S of this tile
+            auto issue_s = [&](auto tile, int ks, bool last, bool end) {
                 constexpr int t = decltype(tile)::value;
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t a = dq + static_cast<uint32_t>(t * (kSlotBytes >> 4));
-                const uint64_t b = dk + static_cast<uint32_t>(slot) * (kSlotBytes >> 4);
+                const uint64_t b = dk + static_cast<uint32_t>(ks) * (kSlotBytes >> 4);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4;
-                        umma_f16(tm + 128u * t, a + off, b + off, id_s, kk > 0);
+                        umma_f16(tmem + 128u * t, a + off, b + off, id_s, kk > 0);
                     }
-                    umma_commit(b0 + 8u * (kBarS + t));
-                    if (last) umma_commit(b0 + 8u * (kBarEmpty + slot));
+                    commit(kBarS + t);
+                    if (last) commit(kBarEmpty + ks);
+                    if (end) commit(kBarQE + t);
                 }
                 __syncwarp();
             };
-            // half h of PV of tile t from the V at `slot`
-            auto issue_pv = [&](auto tile, int h, bool first) {
+            // PV of tile t from the V at `vs`: each half of P as it comes
+            auto issue_pv = [&](auto tile, int vs, uint32_t turn, bool first, bool last) {
                 constexpr int t = decltype(tile)::value;
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t b = dv + static_cast<uint32_t>(slot) * (kSlotBytes >> 4) + static_cast<uint32_t>(h * 4 * (2048 >> 4));
-                if (leader) {
+                const uint64_t b = dv + static_cast<uint32_t>(vs) * (kSlotBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_f16_ta(tm + 256u + 128u * t, tm + 128u * t + 32u * h + 8u * kk,
-                                    b + static_cast<uint32_t>(kk * (2048 >> 4)), id_o, !(first && kk == 0));
+                for (int h = 0; h < 2; ++h) {
+                    wait(kBarP + 2 * t + h, turn);
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            umma_f16_ta(tmem + 256u + 128u * t, tmem + 128u * t + 8u * kk,
+                                        b + static_cast<uint32_t>(kk * (2048 >> 4)), id_o, !(first && kk == 0));
+                        if (h == 1) {
+                            commit(kBarO + t);
+                            if (last) commit(kBarEmpty + vs);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             };
             using Tile0 = std::integral_constant<int, 0>;
             using Tile1 = std::integral_constant<int, 1>;
-            const bool act0 = m_n0 > m_j0, act1 = m_n1 > m_j0;
-            if (act0) wait(kBarQ, 0);
-            wait(kBarFull, 0);
-            if (act0) issue_s(Tile0{}, !act1);
-            if (act1) {
-                wait(kBarQ + 1, 0);
-                issue_s(Tile1{}, true);
-            }
-            next_slot();
-            uint32_t turn = 0;                   // parity of the tile's number
-            for (int j = m_j0; ok && j < m_n; ++j, turn ^= 1u) {
-                // `slot` is V of tile j; the next one is K of tile j + 1
-                const int v_slot = slot;
-                const uint32_t v_use = use;
-                const bool more0 = j + 1 < m_n0, more1 = j + 1 < m_n1;
-                wait(kBarFull + v_slot, v_use);
-                if (j >= m_guard) {              // some row's limit falls in this tile
-                    const int g = (j - m_guard) & 3;
-                    if (leader) mbar_arrive(b0 + 8u * (kBarG + g));
-                    __syncwarp();
-                    wait(kBarV + g, ((j - m_guard) >> 2) & 1);
+            for (int k = 0; ok; ++k) {
+                wait(kBarWF + k % kWorks, (k / kWorks) & 1);
+                if (!ok) break;
+                const Work* w = work_at(k);
+                const int n0 = uniform(w->n[0]), n1 = uniform(w->n[1]), j0 = uniform(w->j0), guard = uniform(w->guard);
+                const bool stop = uniform(w->b) < 0;
+                if (leader) mbar_arrive(b0 + 8u * (kBarWE + k % kWorks));
+                __syncwarp();
+                if (stop) break;
+                const int n = max(n0, n1);
+                if (n <= j0) continue;
+                const bool act0 = n0 > j0, act1 = n1 > j0;
+                wait(kBarFull + slot, use);
+                if (act0) {
+                    wait(kBarQ, items0 & 1);
+                    issue_s(Tile0{}, slot, !act1, j0 + 1 >= n0);
+                }
+                if (act1) {
+                    wait(kBarQ + 1, items1 & 1);
+                    issue_s(Tile1{}, slot, true, j0 + 1 >= n1);
                 }
                 next_slot();
-                const int k_slot = slot;
-                const uint32_t k_use = use;
-                if (j < m_n0) {
-                    slot = v_slot;
-                    wait(kBarP, turn);
-                    issue_pv(Tile0{}, 0, j == m_j0);
-                    wait(kBarP + 1, turn);
-                    issue_pv(Tile0{}, 1, false);
-                    if (ok && leader) {
-                        umma_commit(b0 + 8u * kBarO);
-                        if (j >= m_n1) umma_commit(b0 + 8u * (kBarEmpty + v_slot));
+                // O's place: read out by the softmax warps of the item before
+                for (int j = j0; ok && j < n; ++j) {
+                    // `slot` is V of tile j, the entry behind it K of tile j + 1
+                    const int vs = slot;
+                    const bool more0 = j + 1 < n0, more1 = j + 1 < n1;
+                    wait(kBarFull + vs, use);
+                    if (j >= guard) {                // some row's limit falls in this tile
+                        const int g = guarded & 3;
+                        if (leader) mbar_arrive(b0 + 8u * (kBarG + g));
+                        __syncwarp();
+                        wait(kBarV + g, (guarded >> 2) & 1);
+                        ++guarded;
                     }
-                    __syncwarp();
-                    slot = k_slot;
-                    if (more0) {
-                        wait(kBarFull + k_slot, k_use);
-                        issue_s(Tile0{}, !more1);
+                    next_slot();
+                    const int ks = slot;
+                    if (j < n0) {
+                        if (j == j0 && items0 > 0) wait(kBarOF, (items0 - 1) & 1);
+                        issue_pv(Tile0{}, vs, turn0, j == j0, j >= n1);
+                        turn0 ^= 1u;
+                        if (more0) {
+                            wait(kBarFull + ks, use);
+                            issue_s(Tile0{}, ks, !more1, j + 2 >= n0);
+                        }
                     }
+                    if (j < n1) {
+                        if (j == j0 && items1 > 0) wait(kBarOF + 1, (items1 - 1) & 1);
+                        issue_pv(Tile1{}, vs, turn1, j == j0, true);
+                        turn1 ^= 1u;
+                        if (more1) {
+                            if (!more0) wait(kBarFull + ks, use);
+                            issue_s(Tile1{}, ks, true, j + 2 >= n1);
+                        }
+                    }
+                    if (more0 || more1) next_slot();
                 }
-                if (j < m_n1) {
-                    slot = v_slot;
-                    wait(kBarP + 2, turn);
-                    issue_pv(Tile1{}, 0, j == m_j0);
-                    wait(kBarP + 3, turn);
-                    issue_pv(Tile1{}, 1, false);
-                    if (ok && leader) {
-                        umma_commit(b0 + 8u * (kBarO + 1));
-                        umma_commit(b0 + 8u * (kBarEmpty + v_slot));
-                    }
-                    __syncwarp();
-                    slot = k_slot;
-                    if (more1) {
-                        if (!more0) wait(kBarFull + k_slot, k_use);
-                        issue_s(Tile1{}, true);
-                    }
-                }
-                slot = k_slot;
-                use = k_use;
-                next_slot();
+                items0 += act0;
+                items1 += act1;
             }
-            if (leader) umma_commit(b0 + 8u * kBarDrain);
+            if (leader) commit(kBarDrain);
             __syncwarp();
             wait_bar_warp(b0 + 8u * kBarDrain, 0, abort_flag);
-        }
-    } else if (warp == 10) {
-        // ---- guard of V in the tiles where some row's limit falls
-        for (int j = max(j0, w.guard); j < n; ++j) {
-            const int i = 2 * (j - j0) + 1, s = i % kSlots;
-            // (the MMA thread says when: a warp that waits for a phase of the ring's
-            // barrier long before it begins would take an older phase for it)
-            const uint32_t x4 = (j - w.guard) & 3, par = ((j - w.guard) >> 2) & 1;
-            const bool ok = wait_bar(bar(kBarG + x4), par, abort_flag) &&
-                            wait_bar(bar(kBarFull + s), (i / kSlots) & 1, abort_flag);
-            if (!__all_sync(kFullMask, ok)) break;
-            uint8_t* v = smem + kOffRing + s * kSlotBytes;
-            const int rows = min(kTile, w.nk - j * kTile);   // of this sequence
-            bool bad = false;
+        } else if (warp == 10) {
+            // ---- guard of V in the tiles where some row's limit falls
+            bool ok = true;
+            int guarded = 0, i = 0;                  // tiles guarded, ring entries before the item
+            for (int k = 0; ok; ++k) {
+                ok = wait_bar_warp(bar(kBarWF + k % kWorks), (k / kWorks) & 1, abort_flag);
+                if (!ok) break;
+                const Work w = *work_at(k);
+                if (w.b < 0) break;
+                const int n = max(w.n[0], w.n[1]);
+                for (int j = max(w.j0, w.guard); ok && j < n; ++j, ++guarded) {
+                    const int e = i + 2 * (j - w.j0) + 1, s = e % kSlots;
+                    // (the MMA warp says when: a warp that waits for a phase of the ring's
+                    // barrier long before it begins would take an older phase for it)
+                    ok = wait_bar_warp(bar(kBarG + (guarded & 3)), (guarded >> 2) & 1, abort_flag) &&
+                         wait_bar_warp(bar(kBarFull + s), (e / kSlots) & 1, abort_flag);
+                    if (!ok) break;
+                    uint8_t* v = smem + kOffRing + s * kSlotBytes;
+                    const int rows = min(kTile, w.nk - j * kTile);   // of this sequence
+                    bool bad = false;
 #pragma unroll 8
-            for (int x = lane; x < kSlotBytes / 16; x += 32) {
-                uint4* at = reinterpret_cast<uint4*>(v) + x;
-                if (((x >> 3) & (kTile - 1)) < rows) bad |= any_special<T>(*at);
-                else *at = make_uint4(0u, 0u, 0u, 0u);
+                    for (int x = lane; x < kSlotBytes / 16; x += 32) {
+                        uint4* at = reinterpret_cast<uint4*>(v) + x;
+                        if (((x >> 3) & (kTile - 1)) < rows) bad |= any_special<T>(*at);
+                        else *at = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (bad) special[k % kWorks] = 1;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarV + (guarded & 3)));
+                }
+                i += 2 * max(n - w.j0, 0);
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(bar(kBarWE + k % kWorks));
             }
-            if (bad) *special = 1;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarV + x4));
+        } else if (warp == 11) {
+            // ---- dealer
+            Dealer dealer;
+            dealer.start(p, reinterpret_cast<int*>(smem + kOffLens), lane, blockIdx.x == 0);
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                if (k >= kWorks) ok = wait_bar_warp(bar(kBarWE + k % kWorks), (k / kWorks - 1) & 1, abort_flag);
+                if (!ok) break;
+                Work w;
+                // back and forth over the CTAs
+                const int64_t at = k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+                dealer.item(p, static_cast<int64_t>(k) * gridDim.x + at, lane, w);
+                if (lane == 0) {
+                    *work_at(k) = w;
+                    special[k % kWorks] = 0;
+                    mbar_arrive(bar(kBarWF + k % kWorks));
+                }
+                __syncwarp();
+                if (w.b < 0) break;
+            }
+            if (blockIdx.x == 0) dealer.report_all(p, lane);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax of tile t, a thread per row
         const int t = warp >> 2, r = threadIdx.x & 127;
-        const int i = w.pos[t] + r;
-        const bool real = i < w.nq;
-        const int seen = real ? seen_by(p, w.nq, w.nk, i) : 0;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * t, to = tmem + lanes + 256u + 128u * t;
         const float sc = p.scale_log2;
-        float m = -INFINITY, l = 0.f;
+        uint32_t walked = 0;                     // key tiles over all items: parities of S and O
         bool ok = true;
+        for (int k = 0; ok; ++k) {
+            ok = __all_sync(kFullMask, wait_bar(bar(kBarWF + k % kWorks), (k / kWorks) & 1, abort_flag));
+            if (!ok) break;
+            const Work& w = *work_at(k);         // stays until this warp's arrival below
+            if (w.b < 0) break;
+            const int i = w.pos[t] + r;
+            const bool real = i < w.nq;
+            const int seen = real ? seen_by(p, w.nq, w.nk, i) : 0;
+            const int j0 = w.j0, jn = w.n[t];
+            float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-        for (int j = j0; j < w.n[t]; ++j) {
-            const int x = j - j0;
-            ok = __all_sync(kFullMask, wait_bar(bar(kBarS + t), x & 1, abort_flag));
+            for (int j = j0; j < jn; ++j, ++walked) {
+                ok = __all_sync(kFullMask, wait_bar(bar(kBarS + t), walked & 1, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t lo[64], hi[64];         // the row's scores
+                tmem_ld64(ts, lo);
+                tmem_wait_ld();
+                tmem_ld64(ts + 64u, hi);
+                const int lim = seen - j * kTile;
+                const bool masked = __any_sync(kFullMask, lim < kTile);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) lo[c] = c < lim ? lo[c] : 0xff800000u;
+                }
+                float mx[4];
+                row_max<true>(lo, mx);
+                tmem_wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) hi[c] = c + 64 < lim ? hi[c] : 0xff800000u;
+                }
+                row_max<false>(hi, mx);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                if (__any_sync(kFullMask, top > m + kLazy)) {
+                    const float mn = fmaxf(m, top);
+                    const float a = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
+                    m = mn;
+                    l *= a;
+                    if (j > j0) {                // O of the tiles before takes the new reference
+                        ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), (walked - 1) & 1, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < kHeadDim; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tmem_st32(to + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pw[32];
+                    weights<T>(h == 0 ? lo : hi, sc, -mu, pw, sum);
+                    tmem_st32(ts + 32u * h, pw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarP + 2 * t + h));
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            }
+            if (!ok) break;
+            // ---- the result of a row, or its state (u, m, l) where the keys are split
+            const bool done = jn > j0;           // this query tile walked some key tiles
+            if (done) ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), (walked - 1) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            float s[kTile];
-            {
-                uint32_t (&lo)[64] = *reinterpret_cast<uint32_t(*)[64]>(s);
-                uint32_t (&hi)[64] = *reinterpret_cast<uint32_t(*)[64]>(s + 64);
-                tmem_ld64(ts, lo);
-                tmem_ld64(ts + 64u, hi);
-                tmem_wait_ld();
-            }
-            const int lim = seen - j * kTile;
-            if (__any_sync(kFullMask, lim < kTile)) {
-#pragma unroll
-                for (int c = 0; c < kTile; ++c) s[c] = c < lim ? s[c] : -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int c = 4; c < kTile; c += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = c + e + 4 < kTile ? fmaxf(mx[e], fmaxf(s[c + e], s[c + e + 4])) : fmaxf(mx[e], s[c + e]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-            if (__any_sync(kFullMask, top > m + kLazy)) {
-                const float mn = fmaxf(m, top);
-                const float a = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
-                m = mn;
-                l *= a;
-                if (x > 0) {                     // O of the tiles before takes the new reference
-                    ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), (x - 1) & 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < kHeadDim; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                        tmem_st32(to + c, o);
-                    }
-                    tmem_wait_st();
-                }
-            }
-            const float mu = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t pw[32];
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) {
-                    const float a = fast_exp2(fmaf(s[64 * h + c], sc, -mu));
-                    const float b = fast_exp2(fmaf(s[64 * h + c + 1], sc, -mu));
-                    sum[c & 3] += a;
-                    sum[(c & 3) + 1] += b;
-                    pw[c / 2] = pack2<T>(a, b);
-                }
-                tmem_st32(ts + 32u * h, pw);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarP + 2 * t + h));
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        }
-        // ---- the result of a row, or its state (u, m, l) where the keys are split
-        const int done = w.n[t] - j0;            // key tiles this query tile walked
-        if (ok && done > 0) ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), (done - 1) & 1, abort_flag));
-        tc_fence_after();
-        // the guard ends before the last PV, which the wait above covered
-        if (ok && *special != 0) {
-            for (int rr = 0; rr < 32; ++rr) {
-                const int ii = w.pos[t] + (warp & 3) * 32 + rr;
-                if (ii < w.nq) plain_row<T>(p, w, t, ii, lane);
-            }
-        } else if (ok) {
-            const bool empty = seen <= j0 * kTile || done <= 0;
+            // (the guard ends before the last PV, which the wait above covered)
+            const bool again = special[k % kWorks] != 0;
+            const bool empty = seen <= j0 * kTile || !done;
             const float inv = empty ? 0.f : 1.f / l;
             const int64_t row = out_row(p, w, t, i);
             const int64_t at = row * p.n_splits + w.split;
 #pragma unroll 1
             for (int c = 0; c < kHeadDim; c += 16) {
                 float o[16];
-                if (done > 0) {
+                if (done) {
                     tmem_ld16(to + c, *reinterpret_cast<uint32_t(*)[16]>(o));
                     tmem_wait_ld();
                 }
-                if (!real) continue;
+                if (!real || again) continue;
                 if (p.n_splits == 1) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : o[e] * inv;
@@ -665,12 +849,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                        : make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
-            if (real && p.n_splits == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (done && lane == 0) mbar_arrive(bar(kBarOF + t));
+            if (again) {
+                for (int rr = 0; rr < 32; ++rr) {
+                    const int ii = w.pos[t] + (warp & 3) * 32 + rr;
+                    if (ii < w.nq) plain_row<T>(p, w, t, ii, lane);
+                }
+            } else if (real && p.n_splits == 1) {
                 if (p.lse != nullptr) p.lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
             } else if (real) {
                 p.ws_m[at] = empty ? -INFINITY : m;
                 p.ws_l[at] = empty ? 0.f : l;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarWE + k % kWorks));
         }
         tc_fence_before();
     }
@@ -685,8 +879,11 @@ __global__ void __launch_bounds__(256) fd_prompt_join_kernel(const PromptParams 
     grid_dependency_trigger();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int s_lens[8][2 * (kSorted + 1)];
+    Dealer dealer;
+    dealer.start(p, s_lens[warp], lane, false);
     Work w;
-    find_work(p, static_cast<int64_t>(blockIdx.x) * p.n_splits, lane, w, false);
+    dealer.item(p, static_cast<int64_t>(blockIdx.x) * p.n_splits, lane, w);
     if (w.b < 0) return;
     const int S = p.n_splits;
     for (int x = blockIdx.y * 8 + warp; x < 2 * kTile; x += 8 * gridDim.y) {
@@ -726,8 +923,11 @@ cudaError_t launch_prompt_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, cons
         if (ctx != 0) configured_ctx.store(ctx, std::memory_order_release);
     }
     const int64_t units = tiles * p.head_units;
-    cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(units * p.n_splits)), dim3(kPromptThreads), kSmem, stream,
-                               tmQ, tmK, tmV, p);
+    const int64_t items = units * p.n_splits;
+    const int sms = fd_num_sms(-1);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kPromptThreads), kSmem,
+                               stream, tmQ, tmK, tmV, p);
     if (e != cudaSuccess || p.n_splits == 1) return e;
     return launch_pdl(fd_prompt_join_kernel, dim3(static_cast<unsigned>(units), 8), dim3(256), 0, stream, p);
 }
