@@ -84,7 +84,7 @@ enum Bar : int {
     kBarEmpty = kBarFull + kSlots,
     kBarS = kBarEmpty + kSlots, // [2] S written (MMA commit)
     kBarP = kBarS + 2,          // [2 tiles][2 halves] P written (and O rescaled), one arrival per warp
-    kBarO = kBarP + 4,          // [2] PV done (MMA commit)
+    kBarO = kBarP + 4,          // [2] an item's last PV done (MMA commit)
     kBarOF = kBarO + 2,         // [2] an item's O read out, one arrival per warp
     kBarG = kBarOF + 2,         // [4] a masked tile's V landed and waits for the guard, by its number mod 4
     kBarV = kBarG + 4,          // [4] it is guarded
@@ -100,6 +100,12 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     atomicOr(&g_status, kStatusTimeoutBit);
     *abort_flag = 1;
     return false;
+}
+
+// A descriptor moved on by `off` 16-byte units (no operand crosses 256 KB, so
+// the low word never carries).
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t off) {
+    return (d & 0xffffffff00000000ull) | (static_cast<uint32_t>(d) + off);
 }
 
 // A value that every lane has, known to the compiler as warp-uniform.
@@ -574,42 +580,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             uint32_t turn0 = 0, turn1 = 0;           // parities: P of tile 0, 1,
             int items0 = 0, items1 = 0;              // items in which tile 0, 1 ran
             int guarded = 0;
-            // S of tile t from the K at `ks`; `last`: its last reader; `end`: the item's last S of this tile
-            auto issue_s = [&](auto tile, int ks, bool last, bool end) {
+            // (by the elected lane) S of tile t from the K at `ks`
+            auto issue_s = [&](auto tile, int ks) {
                 constexpr int t = decltype(tile)::value;
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t a = dq + static_cast<uint32_t>(t * (kSlotBytes >> 4));
                 const uint64_t b = dk + static_cast<uint32_t>(ks) * (kSlotBytes >> 4);
-                if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4;
-                        umma_f16(tmem + 128u * t, a + off, b + off, id_s, kk > 0);
-                    }
-                    commit(kBarS + t);
-                    if (last) commit(kBarEmpty + ks);
-                    if (end) commit(kBarQE + t);
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32u) >> 4;
+                    umma_f16(tmem + 128u * t, desc_at(dq, t * (kSlotBytes >> 4) + off), desc_at(b, off), id_s, kk > 0);
                 }
-                __syncwarp();
             };
-            // PV of tile t from the V at `vs`: each half of P as it comes
-            auto issue_pv = [&](auto tile, int vs, uint32_t turn, bool first, bool last) {
+            // One tile's turn: PV(j) from the V at `vs`, each half of P as it comes, then
+            // (`more`) S(j + 1) from the K at `ks`.  MMAs run in issue order, so S
+            // overwrites P only after PV has read it, and a softmax warp that sees S(j + 1)
+            // done knows that PV(j) is: O is signalled apart only at an item's end.
+            // last_v, last_k: no other tile reads the slot after this.
+            auto turn = [&](auto tile, int vs, int ks, uint32_t parity, bool first, bool more, bool last_v, bool last_k,
+                            bool end) {
                 constexpr int t = decltype(tile)::value;
                 const uint64_t b = dv + static_cast<uint32_t>(vs) * (kSlotBytes >> 4);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    wait(kBarP + 2 * t + h, turn);
+                    wait(kBarP + 2 * t + h, parity);
                     if (!ok) return;
                     tc_fence_after();
                     if (leader) {
 #pragma unroll
                         for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                            umma_f16_ta(tmem + 256u + 128u * t, tmem + 128u * t + 8u * kk,
-                                        b + static_cast<uint32_t>(kk * (2048 >> 4)), id_o, !(first && kk == 0));
+                            umma_f16_ta(tmem + 256u + 128u * t, tmem + 128u * t + 8u * kk, desc_at(b, kk * (2048 >> 4)),
+                                        id_o, !(first && kk == 0));
                         if (h == 1) {
-                            commit(kBarO + t);
-                            if (last) commit(kBarEmpty + vs);
+                            if (more) {
+                                issue_s(tile, ks);
+                                commit(kBarS + t);
+                                if (last_k) commit(kBarEmpty + ks);
+                                if (end) commit(kBarQE + t);
+                            } else {
+                                commit(kBarO + t);
+                            }
+                            if (last_v) commit(kBarEmpty + vs);
                         }
                     }
                     __syncwarp();
@@ -632,14 +641,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 wait(kBarFull + slot, use);
                 if (act0) {
                     wait(kBarQ, items0 & 1);
-                    issue_s(Tile0{}, slot, !act1, j0 + 1 >= n0);
+                    tc_fence_after();
+                    if (ok && leader) {
+                        issue_s(Tile0{}, slot);
+                        commit(kBarS);
+                        if (!act1) commit(kBarEmpty + slot);
+                        if (j0 + 1 >= n0) commit(kBarQE);
+                    }
+                    __syncwarp();
                 }
                 if (act1) {
                     wait(kBarQ + 1, items1 & 1);
-                    issue_s(Tile1{}, slot, true, j0 + 1 >= n1);
+                    tc_fence_after();
+                    if (ok && leader) {
+                        issue_s(Tile1{}, slot);
+                        commit(kBarS + 1);
+                        commit(kBarEmpty + slot);
+                        if (j0 + 1 >= n1) commit(kBarQE + 1);
+                    }
+                    __syncwarp();
                 }
                 next_slot();
-                // O's place: read out by the softmax warps of the item before
                 for (int j = j0; ok && j < n; ++j) {
                     // `slot` is V of tile j, the entry behind it K of tile j + 1
                     const int vs = slot;
@@ -654,25 +676,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     next_slot();
                     const int ks = slot;
-                    if (j < n0) {
-                        if (j == j0 && items0 > 0) wait(kBarOF, (items0 - 1) & 1);
-                        issue_pv(Tile0{}, vs, turn0, j == j0, j >= n1);
-                        turn0 ^= 1u;
-                        if (more0) {
-                            wait(kBarFull + ks, use);
-                            issue_s(Tile0{}, ks, !more1, j + 2 >= n0);
-                        }
+                    if (more0 || more1) {
+                        wait(kBarFull + ks, use);
+                        next_slot();
                     }
-                    if (j < n1) {
-                        if (j == j0 && items1 > 0) wait(kBarOF + 1, (items1 - 1) & 1);
-                        issue_pv(Tile1{}, vs, turn1, j == j0, true);
-                        turn1 ^= 1u;
-                        if (more1) {
-                            if (!more0) wait(kBarFull + ks, use);
-                            issue_s(Tile1{}, ks, true, j + 2 >= n1);
-                        }
+                    if (j == j0) {                   // O's places: read out by the softmax warps
+                        if (act0 && items0 > 0) wait(kBarOF, (items0 - 1) & 1);
+                        if (act1 && items1 > 0) wait(kBarOF + 1, (items1 - 1) & 1);
                     }
-                    if (more0 || more1) next_slot();
+                    if (j < n0) turn(Tile0{}, vs, ks, turn0, j == j0, more0, j >= n1, !more1, j + 2 >= n0), turn0 ^= 1u;
+                    if (j < n1) turn(Tile1{}, vs, ks, turn1, j == j0, more1, true, true, j + 2 >= n1), turn1 ^= 1u;
                 }
                 items0 += act0;
                 items1 += act1;
@@ -746,7 +759,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * t, to = tmem + lanes + 256u + 128u * t;
         const float sc = p.scale_log2;
-        uint32_t walked = 0;                     // key tiles over all items: parities of S and O
+        uint32_t walked = 0, ran = 0;            // key tiles, and items with any: parities of S and O
         bool ok = true;
         for (int k = 0; ok; ++k) {
             ok = __all_sync(kFullMask, wait_bar(bar(kBarWF + k % kWorks), (k / kWorks) & 1, abort_flag));
@@ -787,10 +800,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     const float a = fast_exp2(m - (mn == -INFINITY ? 0.f : mn));
                     m = mn;
                     l *= a;
-                    if (j > j0) {                // O of the tiles before takes the new reference
-                        ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), (walked - 1) & 1, abort_flag));
-                        if (!ok) break;
-                        tc_fence_after();
+                    if (j > j0) {                // O, which holds the tiles before, takes the new reference
 #pragma unroll 1
                         for (int c = 0; c < kHeadDim; c += 32) {
                             uint32_t o[32];
@@ -820,7 +830,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!ok) break;
             // ---- the result of a row, or its state (u, m, l) where the keys are split
             const bool done = jn > j0;           // this query tile walked some key tiles
-            if (done) ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), (walked - 1) & 1, abort_flag));
+            if (done) ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), ran++ & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
             // (the guard ends before the last PV, which the wait above covered)
