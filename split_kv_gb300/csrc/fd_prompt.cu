@@ -20,7 +20,7 @@
 // its row of S from tensor memory, writes P (16 bits; the sums l keep the
 // unrounded weights) over it, in two halves so that PV starts on the first
 // while the second is computed.  Warp 8 streams K and V tiles with TMA through
-// a ring of five 32 KB slots, warp 9 issues the MMAs: while one tile's softmax
+// a ring of four 32 KB slots, warp 9 issues the MMAs: while one tile's softmax
 // runs, the tensor cores work on the other tile's PV and next S.  Warp 10 guards
 // the masked tiles (below), warp 11 hands out the items.
 // Tensor memory (512 columns): S/P of tile 0, 1 at 0, 128; O at 256, 384.
@@ -34,10 +34,11 @@
 //
 // Masked places: scores past a row's limit are replaced by -inf before they
 // are used, so what K holds there does not matter.  P is 0 there, but 0 * NaN
-// is NaN, so in the (last) tiles where some row's limit falls, warp 10 zeroes
-// the V rows past the sequence's end and looks for infinities and NaN in the
-// others; only if it finds one are the item's rows computed again by a plain
-// loop over the keys each row sees.
+// is NaN: V's rows past the sequence's end are zeroed in shared memory in the
+// one tile that has some (warp 10), and a row of O that comes out with an
+// infinity or NaN is looked into: if a key that the row does not see but whose
+// tile it walked has one in V, the row is computed again by a plain loop over
+// the keys that it sees.
 //
 // Bound by the tensor cores when sequences are long: 4 * 128 flops per visible
 // pair and head against 2 bytes per element read once.
@@ -60,17 +61,17 @@ __device__ unsigned int g_status = 0;   // this file's bits of the device status
 constexpr unsigned kFullMask = 0xffffffffu;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kTile = 128;              // queries per tile, keys per tile
-constexpr int kSlots = 5;
+constexpr int kSlots = 4;
 constexpr int kSlotBytes = kTile * 256; // [128 x 64 dims] low half, high half
 constexpr int kHalf = kSlotBytes / 2;
 constexpr int kOffRing = 2 * kSlotBytes;
-constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+constexpr int kOffStage = kOffRing + kSlots * kSlotBytes;   // the epilogue's, 4 KB a softmax warp
+constexpr int kOffBar = kOffStage + 8 * 4096;
 constexpr int kOffWork = kOffBar + 384; // [kWorks] Work, 64 bytes each
 constexpr int kWorks = 4;
-constexpr int kOffMisc = kOffWork + kWorks * 64;    // tensor memory address, abort flag, [kWorks] special flags
-constexpr int kOffLens = kOffMisc + 32; // cu_q and cu_k of up to kSorted sequences
+constexpr int kOffMisc = kOffWork + kWorks * 64;    // tensor memory address, abort flag
 constexpr int kSorted = 128;            // batches up to this are handed out largest first
-constexpr int kSmem = kOffLens + 2 * (kSorted + 1) * 4 + 1024;
+constexpr int kSmem = kOffMisc + 32 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr int kPromptThreads = 12 * 32;
 constexpr float kLazy = 8.f;
@@ -86,9 +87,9 @@ enum Bar : int {
     kBarP = kBarS + 2,          // [2 tiles][2 halves] P written (and O rescaled), one arrival per warp
     kBarO = kBarP + 4,          // [2] an item's last PV done (MMA commit)
     kBarOF = kBarO + 2,         // [2] an item's O read out, one arrival per warp
-    kBarG = kBarOF + 2,         // [4] a masked tile's V landed and waits for the guard, by its number mod 4
-    kBarV = kBarG + 4,          // [4] it is guarded
-    kBarWF = kBarV + 4,         // [kWorks] an item is handed out
+    kBarG = kBarOF + 2,         // the V of a tile with a sequence's end landed
+    kBarV = kBarG + 1,          // its rows past the end are zero
+    kBarWF = kBarV + 1,         // [kWorks] an item is handed out
     kBarWE = kBarWF + kWorks,   // [kWorks] every role is done with it: producer, MMA, guard, 8 softmax warps
     kBarDrain = kBarWE + kWorks,// every MMA done
     kBars
@@ -137,7 +138,7 @@ struct Work {
     int head[2], pos[2];        // of the two query tiles
     int n[2];                   // key tiles each sees, from 0 (<= j0: inactive)
     int j0, j1;                 // key tiles of this split
-    int guard;                  // first key tile where some row's limit falls
+    int tail;                   // the key tile where the sequence ends, past the last one if that is full
     int split;
 };
 static_assert(sizeof(Work) <= 64, "work");
@@ -146,7 +147,8 @@ __device__ __forceinline__ int seen_by(const PromptParams& p, int nq, int nk, in
     return p.causal ? min(max(nk - nq + 1 + i, 0), nk) : nk;
 }
 
-__device__ __forceinline__ int span_of(const PromptParams& p) { return p.pair_heads ? kTile : 2 * kTile; }
+__device__ __forceinline__ int span_shift(const PromptParams& p) { return p.pair_heads ? 7 : 8; }
+static_assert(kTile == 1 << 7, "span_shift");
 
 // Whether a sequence's offsets hold; its numbers of queries and keys.
 __device__ __forceinline__ bool read_seq(const PromptParams& p, const int* cq, const int* ck, int& q0, int& nq, int& k0,
@@ -160,138 +162,150 @@ __device__ __forceinline__ bool read_seq(const PromptParams& p, const int* cq, c
 
 // The item (tile `tile` of the sequence in w, head unit, split): the rest of w.
 __device__ __forceinline__ void fill_work(const PromptParams& p, int tile, int unit, int split, Work& w) {
-    const int span = span_of(p);
     w.split = split;
     int most = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         w.head[t] = p.pair_heads ? 2 * unit + t : unit;
-        w.pos[t] = tile * span + (p.pair_heads ? 0 : t * kTile);
+        w.pos[t] = (tile << span_shift(p)) + (p.pair_heads ? 0 : t * kTile);
         const int last = min(w.pos[t] + kTile, w.nq) - 1;
         const int keys = last >= w.pos[t] ? seen_by(p, w.nq, w.nk, last) : 0;
         w.n[t] = (keys + kTile - 1) / kTile;
         most = max(most, w.n[t]);
     }
-    const int each = most / p.n_splits, more = most % p.n_splits;
-    w.j0 = split * each + min(split, more);
-    w.j1 = w.j0 + each + (split < more ? 1 : 0);
+    w.j0 = 0;
+    w.j1 = most;
+    if (p.n_splits > 1) {
+        const int each = most / p.n_splits, more = most % p.n_splits;
+        w.j0 = split * each + min(split, more);
+        w.j1 = w.j0 + each + (split < more ? 1 : 0);
+    }
     w.n[0] = min(w.n[0], w.j1);
     w.n[1] = min(w.n[1], w.j1);
-    w.guard = max(w.j0, seen_by(p, w.nq, w.nk, w.pos[0]) / kTile);
+    w.tail = w.nk % kTile != 0 ? w.nk / kTile : INT32_MAX;
 }
 
 // Hands out items by their rank, one warp.  Ranks count (query tile, head unit,
 // split), splits fastest.  Up to kSorted sequences (sorted): tiles in order of
-// the key tiles they see, most first; beyond: as the sequences come, each
-// one's last tile first (ranks have to ascend).
+// the key tiles they see, most first, the lanes holding the sequences' lengths;
+// beyond: as the sequences come, each one's last tile first (ranks have to
+// ascend).
 struct Dealer {
-    const int* cq;              // sorted: shared memory copies
-    const int* ck;
+    static constexpr int kPer = kSorted / 32;
     bool sorted;
+    int q0[kPer], nq[kPer], k0[kPer], nk[kPer];     // sorted: sequences 32 c + lane (lengths 0: none)
     int top;                    // sorted: the most key tiles any sequence has
     int base, before;           // else: the chunk of 32 sequences looked at, tiles before it
 
     // tiles of a sequence that see at least `need` key tiles
-    __device__ __forceinline__ int tiles_seeing(const PromptParams& p, int nq, int nk, int need) const {
-        const int span = span_of(p), tiles = (nq + span - 1) / span;
+    __device__ __forceinline__ int tiles_seeing(const PromptParams& p, int n, int m, int need) const {
+        const int shift = span_shift(p), round = (1 << shift) - 1, tiles = (n + round) >> shift;
         if (need <= 0) return tiles;
-        const int x = (need - 1) * kTile + 1;           // keys
-        if (nk < x) return 0;
+        const int x = (need - 1) * kTile + 1;       // keys
+        if (m < x) return 0;
         if (!p.causal) return tiles;
-        const int rows = x - nk + nq;                    // the first so many rows see fewer
-        return tiles - (rows <= 0 ? 0 : (rows + span - 1) / span - 1);
+        const int rows = x - m + n;                  // the first so many rows see fewer, but for the last of them
+        return rows <= 0 ? tiles : tiles - (((rows + round) >> shift) - 1);
     }
-    __device__ __forceinline__ int all_seeing(const PromptParams& p, int need, int lane) const {
+    __device__ __forceinline__ int all_seeing(const PromptParams& p, int need) const {
         int sum = 0;
-        for (int c = 0; c < p.batch; c += 32) {
-            int q0, nq, k0, nk;
-            if (c + lane < p.batch && read_seq(p, cq + c + lane, ck + c + lane, q0, nq, k0, nk))
-                sum += tiles_seeing(p, nq, nk, need);
-        }
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) sum += tiles_seeing(p, nq[c], nk[c], need);
         return __reduce_add_sync(kFullMask, sum);
     }
-    __device__ __forceinline__ void start(const PromptParams& p, int* shared_lens, int lane, bool report) {
+    __device__ __forceinline__ void start(const PromptParams& p, int lane, bool report) {
         sorted = p.batch <= kSorted;
         base = before = top = 0;
-        cq = p.cu_q;
-        ck = p.cu_k;
         if (!sorted) return;
-        int* sq = shared_lens;
-        int* sk = shared_lens + kSorted + 1;
-        for (int i = lane; i <= p.batch; i += 32) {
-            sq[i] = p.cu_q[i];
-            sk[i] = p.cu_k[i];
-        }
-        __syncwarp();
-        cq = sq;
-        ck = sk;
         int most = 0;
         bool bad = false;
-        for (int c = lane; c < p.batch; c += 32) {
-            int q0, nq, k0, nk;
-            if (read_seq(p, cq + c, ck + c, q0, nq, k0, nk)) most = max(most, (nk + kTile - 1) / kTile);
-            else bad = true;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            const int b = 32 * c + lane;
+            q0[c] = nq[c] = k0[c] = nk[c] = 0;
+            if (b < p.batch && !read_seq(p, p.cu_q + b, p.cu_k + b, q0[c], nq[c], k0[c], nk[c])) {
+                bad = true;
+                nq[c] = nk[c] = 0;
+            }
+            most = max(most, (nk[c] + kTile - 1) / kTile);
         }
         top = __reduce_max_sync(kFullMask, most);
         if (report && bad) atomicOr(&g_status, kStatusSeqlenBit);
     }
-    // (every lane gets the item; b = -1 past the last one)
-    __device__ __forceinline__ void item(const PromptParams& p, int64_t rank, int lane, Work& w) {
-        const int split = static_cast<int>(rank % p.n_splits);
-        const int64_t rest = rank / p.n_splits;
-        const int unit = static_cast<int>(rest % p.head_units);
-        const int64_t at = rest / p.head_units;          // the tile's rank
-        w.b = -1;
-        int need = 0;                                    // key tiles of the tile with that rank
-        int64_t idx = at;
-        if (sorted) {
-            if (at >= all_seeing(p, 0, lane)) return;
-            int hi = top + 1;
-            while (hi - need > 1) {
-                const int mid = (need + hi) >> 1;
-                if (all_seeing(p, mid, lane) > at) need = mid;
-                else hi = mid;
-            }
-            idx = at - all_seeing(p, need + 1, lane);    // among those that see exactly `need`
-            before = 0;
-            base = 0;
-        }
-        for (; base < p.batch; base += 32) {
-            int q0 = 0, nq = 0, k0 = 0, nk = 0, mine = 0, tile0 = 0;
-            if (base + lane < p.batch && read_seq(p, cq + base + lane, ck + base + lane, q0, nq, k0, nk)) {
-                const int all = tiles_seeing(p, nq, nk, 0);
-                const int from = sorted ? tiles_seeing(p, nq, nk, need) : all;
-                mine = sorted ? from - tiles_seeing(p, nq, nk, need + 1) : all;
-                tile0 = all - from;                      // the first of these tiles
-            }
-            int upto = mine;
+    // Among the sequences b, b + lane.. of one chunk with `mine` tiles each, the
+    // one of tile idx - before; false: not in this chunk.
+    __device__ __forceinline__ bool find(int idx, int mine, int& src, int& i) {
+        int upto = mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFullMask, upto, o);
-                if (lane >= o) upto += y;
-            }
-            const unsigned hit = __ballot_sync(kFullMask, idx - before < upto);
-            if (hit != 0) {
-                const int src = __ffs(hit) - 1;
-                const int i = static_cast<int>(idx - before) - (upto - mine);
-                w.b = base + src;
-                w.q0 = __shfl_sync(kFullMask, q0, src);
-                w.nq = __shfl_sync(kFullMask, nq, src);
-                w.k0 = __shfl_sync(kFullMask, k0, src);
-                w.nk = __shfl_sync(kFullMask, nk, src);
-                const int tile = __shfl_sync(kFullMask, sorted ? tile0 + i : mine - 1 - i, src);
-                fill_work(p, tile, unit, split, w);
-                return;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFullMask, upto, o);
+            if ((threadIdx.x & 31) >= o) upto += y;
+        }
+        const unsigned hit = __ballot_sync(kFullMask, idx - before < upto);
+        if (hit == 0) {
             before += __shfl_sync(kFullMask, upto, 31);
+            return false;
+        }
+        src = __ffs(hit) - 1;
+        i = idx - before - __shfl_sync(kFullMask, upto - mine, src);
+        return true;
+    }
+    __device__ __forceinline__ void take(Work& w, int b, int src, int q, int n, int k, int m) {
+        w.b = b + src;
+        w.q0 = __shfl_sync(kFullMask, q, src);
+        w.nq = __shfl_sync(kFullMask, n, src);
+        w.k0 = __shfl_sync(kFullMask, k, src);
+        w.nk = __shfl_sync(kFullMask, m, src);
+    }
+    // (every lane gets the item; b = -1 past the last one)
+    __device__ __forceinline__ void item(const PromptParams& p, uint32_t rank, int lane, Work& w) {
+        int split = 0;
+        if (p.n_splits > 1) {
+            split = static_cast<int>(rank % p.n_splits);
+            rank /= p.n_splits;
+        }
+        const int unit = static_cast<int>(rank % p.head_units);
+        const int at = static_cast<int>(rank / p.head_units);   // the tile's rank
+        w.b = -1;
+        int src, i;
+        if (!sorted) {
+            for (; base < p.batch; base += 32) {
+                int q = 0, n = 0, k = 0, m = 0;
+                const bool ok = base + lane < p.batch && read_seq(p, p.cu_q + base + lane, p.cu_k + base + lane, q, n, k, m);
+                const int mine = ok ? tiles_seeing(p, n, m, 0) : 0;
+                if (find(at, mine, src, i)) {
+                    take(w, base, src, q, n, k, m);
+                    fill_work(p, __shfl_sync(kFullMask, mine, src) - 1 - i, unit, split, w);
+                    return;
+                }
+            }
+            return;
+        }
+        if (at >= all_seeing(p, 0)) return;
+        int need = 0, hi = top + 1;                      // key tiles of the tile with that rank
+        while (hi - need > 1) {
+            const int mid = (need + hi) >> 1;
+            if (all_seeing(p, mid) > at) need = mid;
+            else hi = mid;
+        }
+        const int idx = at - all_seeing(p, need + 1);    // among those that see exactly `need`
+        before = 0;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            const int from = tiles_seeing(p, nq[c], nk[c], need), mine = from - tiles_seeing(p, nq[c], nk[c], need + 1);
+            if (w.b < 0 && find(idx, mine, src, i)) {
+                take(w, 32 * c, src, q0[c], nq[c], k0[c], nk[c]);
+                const int tile0 = tiles_seeing(p, nq[c], nk[c], 0) - from;   // the first of these tiles
+                fill_work(p, __shfl_sync(kFullMask, tile0, src) + i, unit, split, w);
+            }
         }
     }
     // unsorted: offsets of every sequence
     __device__ __forceinline__ void report_all(const PromptParams& p, int lane) const {
         if (sorted) return;
         for (int c = lane; c < p.batch; c += 32) {
-            int q0, nq, k0, nk;
-            if (!read_seq(p, p.cu_q + c, p.cu_k + c, q0, nq, k0, nk)) atomicOr(&g_status, kStatusSeqlenBit);
+            int q, n, k, m;
+            if (!read_seq(p, p.cu_q + c, p.cu_k + c, q, n, k, m)) atomicOr(&g_status, kStatusSeqlenBit);
         }
     }
 };
@@ -338,41 +352,26 @@ __device__ __forceinline__ int64_t out_row(const PromptParams& p, const Work& w,
     return (static_cast<int64_t>(w.q0) + i) * p.n_q_heads + w.head[t];
 }
 
-// N consecutive dims of a row of out, from dim d (a multiple of N, N = 4 or 16)
-template <int N>
-__device__ __forceinline__ void put_out(const PromptParams& p, int64_t row, int d, const float* o) {
+// Four consecutive dims of a row of out, from dim d.
+__device__ __forceinline__ void put_out4(const PromptParams& p, int64_t row, int d, const float (&o)[4]) {
     const int64_t at = row * kHeadDim + d;
     if (p.out_dtype == 2) {
         float* dst = static_cast<float*>(p.out) + at;
-        if (p.out_vec) {
 #pragma unroll
-            for (int e = 0; e < N; e += 4)
-                *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e) dst[e] = o[e];
-        }
+        for (int e = 0; e < 4; ++e) dst[e] = o[e];
         return;
     }
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e)
-        w[e] = p.out_dtype == 0 ? pack2<__half>(o[2 * e], o[2 * e + 1]) : pack2<__nv_bfloat16>(o[2 * e], o[2 * e + 1]);
+    const bool half = p.out_dtype == 0;
+    const uint32_t a = half ? pack2<__half>(o[0], o[1]) : pack2<__nv_bfloat16>(o[0], o[1]);
+    const uint32_t b = half ? pack2<__half>(o[2], o[3]) : pack2<__nv_bfloat16>(o[2], o[3]);
     uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
     if (p.out_vec) {
-        if constexpr (N == 4) {
-            *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < N / 2; e += 4)
-                *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-        }
+        *reinterpret_cast<uint2*>(dst) = make_uint2(a, b);
     } else {
-#pragma unroll
-        for (int e = 0; e < N / 2; ++e) {
-            dst[2 * e] = static_cast<uint16_t>(w[e]);
-            dst[2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
-        }
+        dst[0] = static_cast<uint16_t>(a);
+        dst[1] = static_cast<uint16_t>(a >> 16);
+        dst[2] = static_cast<uint16_t>(b);
+        dst[3] = static_cast<uint16_t>(b >> 16);
     }
 }
 
@@ -408,7 +407,7 @@ __device__ __noinline__ void plain_row(const PromptParams& p, const Work& w, int
     if (p.n_splits == 1) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = empty ? 0.f : o[e] / l;
-        put_out<4>(p, row, 4 * lane, o);
+        put_out4(p, row, 4 * lane, o);
         if (lane == 0 && p.lse != nullptr) p.lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
     } else {
         const int64_t at = row * p.n_splits + w.split;
@@ -463,10 +462,97 @@ __device__ __forceinline__ bool any_special(const uint4& r) {
     return ((((r.x & e) + one) | ((r.y & e) + one) | ((r.z & e) + one) | ((r.w & e) + one)) & 0x80008000u) != 0;
 }
 
+// Whether V has an infinity or NaN in a key tile that some row of this query
+// tile does not see whole (one warp).
+template <typename T>
+__device__ __noinline__ bool hidden_special(const PromptParams& p, const Work& w, int t, int lane) {
+    const int first = max(w.j0 * kTile, seen_by(p, w.nq, w.nk, w.pos[t]) / kTile * kTile);
+    const int last = min(w.n[t] * kTile, w.nk);
+    const int g = w.head[t] / p.group;
+    bool bad = false;
+    for (int j = first + (lane >> 4); j < last; j += 2)
+        bad |= any_special<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + (static_cast<int64_t>(w.k0) + j) * p.v_st +
+                                                              g * p.v_sh + 8 * (lane & 15)));
+    return __any_sync(kFullMask, bad);
+}
+
+// 16 bytes of output at an address that has only its element's alignment
+__device__ __forceinline__ void put_odd(uint8_t* dst, const uint4& q, bool wide) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (wide) {
+            reinterpret_cast<uint32_t*>(dst)[e] = w[e];
+        } else {
+            reinterpret_cast<uint16_t*>(dst)[2 * e] = static_cast<uint16_t>(w[e]);
+            reinterpret_cast<uint16_t*>(dst)[2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
+        }
+    }
+}
+
+// A warp's 32 rows of O, times inv, to rows at0, at0 + row_step, .. of out or of
+// the states u: 64 (16-bit) or 32 (32-bit) dims at a time, each lane's row to the
+// warp's staging area, 128 bytes a row, swizzled; from there eight lanes a row to
+// memory (a lane writing its own row touches 32 lines a store: 3.4 us an item).
+// Returns NaN if an infinity or NaN was among the lane's row, else 0.
+// (One body for both widths: a second one, or a call, cost the softmax loop
+// its registers, and 18 % of the kernel's rate.)
+__device__ __forceinline__ float write_rows(const PromptParams& p, uint8_t* stage, uint32_t to, int64_t at0,
+                                            int64_t row_step, int rows, bool done, bool empty, float inv, int lane) {
+    const bool wide = p.n_splits > 1 || p.out_dtype == 2;
+    const int64_t bytes = wide ? 4 : 2;
+    uint8_t* dst = static_cast<uint8_t*>(p.n_splits > 1 ? static_cast<void*>(p.ws_u) : p.out) +
+                   at0 * kHeadDim * bytes + (lane & 7) * 16;
+    const int64_t step = row_step * kHeadDim * bytes;
+    float odd = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kHeadDim; c += 32) {
+        uint32_t o[32];
+        if (done) {
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float f = empty ? 0.f : __uint_as_float(o[e]) * inv;
+            odd = fmaf(f, 0.f, odd);
+            o[e] = __float_as_uint(f);
+        }
+        int unit = 0;
+        if (!wide) {
+            unit = (c & 32) >> 3;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float a = __uint_as_float(o[2 * e]), b = __uint_as_float(o[2 * e + 1]);
+                o[e] = p.out_dtype == 0 ? pack2<__half>(a, b) : pack2<__nv_bfloat16>(a, b);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (u < 4 || wide)
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((unit + u) ^ (lane & 7)) << 4)) =
+                    make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        if (!wide && (c & 32) == 0) continue;
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const int rr = 4 * y + (lane >> 3);
+            const uint4 q = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            if (rr < rows) {
+                if (p.n_splits > 1 || p.out_vec) *reinterpret_cast<uint4*>(dst + rr * step) = q;
+                else put_odd(dst + rr * step, q, wide);
+            }
+        }
+        dst += 128;
+        __syncwarp();
+    }
+    return odd;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     fd_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const PromptParams p) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -475,7 +561,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     auto bar = [&](int i) { return bar0 + 8u * i; };
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-    volatile int* special = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);   // [kWorks]
     auto work_at = [&](int k) { return reinterpret_cast<Work*>(smem + kOffWork + 64 * (k % kWorks)); };
 
     if (threadIdx.x == 256) {
@@ -579,7 +664,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             };
             uint32_t turn0 = 0, turn1 = 0;           // parities: P of tile 0, 1,
             int items0 = 0, items1 = 0;              // items in which tile 0, 1 ran
-            int guarded = 0;
+            int tails = 0;                           // tiles with a sequence's end
             // (by the elected lane) S of tile t from the K at `ks`
             auto issue_s = [&](auto tile, int ks) {
                 constexpr int t = decltype(tile)::value;
@@ -630,7 +715,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 wait(kBarWF + k % kWorks, (k / kWorks) & 1);
                 if (!ok) break;
                 const Work* w = work_at(k);
-                const int n0 = uniform(w->n[0]), n1 = uniform(w->n[1]), j0 = uniform(w->j0), guard = uniform(w->guard);
+                const int n0 = uniform(w->n[0]), n1 = uniform(w->n[1]), j0 = uniform(w->j0), tail = uniform(w->tail);
                 const bool stop = uniform(w->b) < 0;
                 if (leader) mbar_arrive(b0 + 8u * (kBarWE + k % kWorks));
                 __syncwarp();
@@ -667,12 +752,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     const int vs = slot;
                     const bool more0 = j + 1 < n0, more1 = j + 1 < n1;
                     wait(kBarFull + vs, use);
-                    if (j >= guard) {                // some row's limit falls in this tile
-                        const int g = guarded & 3;
-                        if (leader) mbar_arrive(b0 + 8u * (kBarG + g));
+                    if (j == tail) {                 // the sequence ends in this tile
+                        if (leader) mbar_arrive(b0 + 8u * kBarG);
                         __syncwarp();
-                        wait(kBarV + g, (guarded >> 2) & 1);
-                        ++guarded;
+                        wait(kBarV, tails & 1);
+                        ++tails;
                     }
                     next_slot();
                     const int ks = slot;
@@ -694,56 +778,51 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             __syncwarp();
             wait_bar_warp(b0 + 8u * kBarDrain, 0, abort_flag);
         } else if (warp == 10) {
-            // ---- guard of V in the tiles where some row's limit falls
+            // ---- zeroes V's rows past a sequence's end
             bool ok = true;
-            int guarded = 0, i = 0;                  // tiles guarded, ring entries before the item
+            int tails = 0, i = 0;                    // tiles with an end, ring entries before the item
             for (int k = 0; ok; ++k) {
                 ok = wait_bar_warp(bar(kBarWF + k % kWorks), (k / kWorks) & 1, abort_flag);
                 if (!ok) break;
                 const Work w = *work_at(k);
                 if (w.b < 0) break;
                 const int n = max(w.n[0], w.n[1]);
-                for (int j = max(w.j0, w.guard); ok && j < n; ++j, ++guarded) {
-                    const int e = i + 2 * (j - w.j0) + 1, s = e % kSlots;
+                if (w.tail >= w.j0 && w.tail < n) {
+                    const int e = i + 2 * (w.tail - w.j0) + 1;
                     // (the MMA warp says when: a warp that waits for a phase of the ring's
                     // barrier long before it begins would take an older phase for it)
-                    ok = wait_bar_warp(bar(kBarG + (guarded & 3)), (guarded >> 2) & 1, abort_flag) &&
-                         wait_bar_warp(bar(kBarFull + s), (e / kSlots) & 1, abort_flag);
+                    ok = wait_bar_warp(bar(kBarG), tails & 1, abort_flag) &&
+                         wait_bar_warp(bar(kBarFull + e % kSlots), (e / kSlots) & 1, abort_flag);
                     if (!ok) break;
-                    uint8_t* v = smem + kOffRing + s * kSlotBytes;
-                    const int rows = min(kTile, w.nk - j * kTile);   // of this sequence
-                    bool bad = false;
-#pragma unroll 8
-                    for (int x = lane; x < kSlotBytes / 16; x += 32) {
-                        uint4* at = reinterpret_cast<uint4*>(v) + x;
-                        if (((x >> 3) & (kTile - 1)) < rows) bad |= any_special<T>(*at);
-                        else *at = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    if (bad) special[k % kWorks] = 1;
+                    uint8_t* v = smem + kOffRing + e % kSlots * kSlotBytes;
+                    for (int r = w.nk % kTile + (lane >> 3); r < kTile; r += 4)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<uint4*>(v + h * kHalf + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kBarV + (guarded & 3)));
+                    if (lane == 0) mbar_arrive(bar(kBarV));
+                    ++tails;
                 }
                 i += 2 * max(n - w.j0, 0);
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(bar(kBarWE + k % kWorks));
+                if (lane == 0) mbar_arrive(bar(kBarWE + k % kWorks));
             }
             __syncwarp();
         } else if (warp == 11) {
             // ---- dealer
             Dealer dealer;
-            dealer.start(p, reinterpret_cast<int*>(smem + kOffLens), lane, blockIdx.x == 0);
+            dealer.start(p, lane, blockIdx.x == 0);
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 if (k >= kWorks) ok = wait_bar_warp(bar(kBarWE + k % kWorks), (k / kWorks - 1) & 1, abort_flag);
                 if (!ok) break;
                 Work w;
                 // back and forth over the CTAs
-                const int64_t at = k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-                dealer.item(p, static_cast<int64_t>(k) * gridDim.x + at, lane, w);
+                const uint32_t at = k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+                dealer.item(p, k * gridDim.x + at, lane, w);
                 if (lane == 0) {
                     *work_at(k) = w;
-                    special[k % kWorks] = 0;
                     mbar_arrive(bar(kBarWF + k % kWorks));
                 }
                 __syncwarp();
@@ -833,45 +912,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (done) ok = __all_sync(kFullMask, wait_bar(bar(kBarO + t), ran++ & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            // (the guard ends before the last PV, which the wait above covered)
-            const bool again = special[k % kWorks] != 0;
             const bool empty = seen <= j0 * kTile || !done;
-            const float inv = empty ? 0.f : 1.f / l;
-            const int64_t row = out_row(p, w, t, i);
-            const int64_t at = row * p.n_splits + w.split;
-#pragma unroll 1
-            for (int c = 0; c < kHeadDim; c += 16) {
-                float o[16];
-                if (done) {
-                    tmem_ld16(to + c, *reinterpret_cast<uint32_t(*)[16]>(o));
-                    tmem_wait_ld();
-                }
-                if (!real || again) continue;
-                if (p.n_splits == 1) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = empty ? 0.f : o[e] * inv;
-                    put_out<16>(p, row, c, o);
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(p.ws_u + at * kHeadDim + c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = empty ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                       : make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                }
-            }
+            const float inv = p.n_splits > 1 ? 1.f : 1.f / l;
+            const int rows = min(32, w.nq - w.pos[t] - 32 * (warp & 3));   // of this warp that exist
+            const int64_t row0 = out_row(p, w, t, i - lane);
+            const int64_t row_step = p.n_splits > 1 ? static_cast<int64_t>(p.n_q_heads) * p.n_splits : p.n_q_heads;
+            const int64_t at0 = p.n_splits > 1 ? row0 * p.n_splits + w.split : row0;   // rows of out, or of the states
+            const float odd = write_rows(p, smem + kOffStage + warp * 4096, to, at0, row_step, rows, done, empty, inv, lane);
             tc_fence_before();
             __syncwarp();
             if (done && lane == 0) mbar_arrive(bar(kBarOF + t));
-            if (again) {
-                for (int rr = 0; rr < 32; ++rr) {
-                    const int ii = w.pos[t] + (warp & 3) * 32 + rr;
-                    if (ii < w.nq) plain_row<T>(p, w, t, ii, lane);
-                }
-            } else if (real && p.n_splits == 1) {
-                if (p.lse != nullptr) p.lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && p.n_splits == 1) {
+                if (p.lse != nullptr) p.lse[at0 + lane * row_step] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
             } else if (real) {
-                p.ws_m[at] = empty ? -INFINITY : m;
-                p.ws_l[at] = empty ? 0.f : l;
+                p.ws_m[at0 + lane * row_step] = empty ? -INFINITY : m;
+                p.ws_l[at0 + lane * row_step] = empty ? 0.f : l;
+            }
+            // rows that a value they do not see may have reached
+            unsigned again = __ballot_sync(kFullMask, real && odd != odd);
+            if (again != 0 && hidden_special<T>(p, w, t, lane)) {
+                __syncwarp();
+                for (; again != 0; again &= again - 1)
+                    plain_row<T>(p, w, t, w.pos[t] + 32 * (warp & 3) + __ffs(again) - 1, lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarWE + k % kWorks));
@@ -885,15 +947,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 // Joins the splits of each row: M = max m_s, out = sum 2^(m_s - M) u_s / L,
 // L = sum 2^(m_s - M) l_s, in split order.  The blocks of the split kernel
 // without its splits; a warp per row, 4 dims a lane.
-__global__ void __launch_bounds__(256) fd_prompt_join_kernel(const PromptParams p) {
+__global__ void __launch_bounds__(256) fd_prompt_join_kernel(const __grid_constant__ PromptParams p) {
     grid_dependency_trigger();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ int s_lens[8][2 * (kSorted + 1)];
     Dealer dealer;
-    dealer.start(p, s_lens[warp], lane, false);
+    dealer.start(p, lane, false);
     Work w;
-    dealer.item(p, static_cast<int64_t>(blockIdx.x) * p.n_splits, lane, w);
+    dealer.item(p, blockIdx.x * static_cast<uint32_t>(p.n_splits), lane, w);
     if (w.b < 0) return;
     const int S = p.n_splits;
     for (int x = blockIdx.y * 8 + warp; x < 2 * kTile; x += 8 * gridDim.y) {
@@ -916,7 +977,7 @@ __global__ void __launch_bounds__(256) fd_prompt_join_kernel(const PromptParams 
         const bool empty = seen_by(p, w.nq, w.nk, i) == 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = empty ? 0.f : o[e] / L;
-        put_out<4>(p, row, 4 * lane, o);
+        put_out4(p, row, 4 * lane, o);
         if (lane == 0 && p.lse != nullptr) p.lse[row] = empty ? -INFINITY : (M + log2f(L)) * kLn2;
     }
 }
