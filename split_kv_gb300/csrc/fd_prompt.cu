@@ -408,7 +408,7 @@ __device__ __noinline__ void plain_row(const PromptParams& p, const Work& w, int
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = empty ? 0.f : o[e] / l;
         put_out4(p, row, 4 * lane, o);
-        if (lane == 0 && p.lse != nullptr) p.lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (lane == 0 && p.lse != nullptr) p.lse[row] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
     } else {
         const int64_t at = row * p.n_splits + w.split;
         *reinterpret_cast<float4*>(p.ws_u + at * kHeadDim + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
@@ -504,7 +504,9 @@ __device__ __forceinline__ float write_rows(const PromptParams& p, uint8_t* stag
     uint8_t* dst = static_cast<uint8_t*>(p.n_splits > 1 ? static_cast<void*>(p.ws_u) : p.out) +
                    at0 * kHeadDim * bytes + (lane & 7) * 16;
     const int64_t step = row_step * kHeadDim * bytes;
-    float odd = 0.f;
+    const float2 inv2 = make_float2(inv, inv), none = make_float2(0.f, 0.f);
+    const bool some_empty = __any_sync(kFullMask, empty);
+    float2 odd = none;
 #pragma unroll 1
     for (int c = 0; c < kHeadDim; c += 32) {
         uint32_t o[32];
@@ -512,26 +514,40 @@ __device__ __forceinline__ float write_rows(const PromptParams& p, uint8_t* stag
             tmem_ld32(to + c, o);
             tmem_wait_ld();
         }
+        if (some_empty) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const float f = empty ? 0.f : __uint_as_float(o[e]) * inv;
-            odd = fmaf(f, 0.f, odd);
-            o[e] = __float_as_uint(f);
+            for (int e = 0; e < 32; ++e) o[e] = empty ? 0u : o[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            const float2 f = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), inv2);
+            odd = __ffma2_rn(f, none, odd);
+            o[e] = __float_as_uint(f.x);
+            o[e + 1] = __float_as_uint(f.y);
         }
         int unit = 0;
         if (!wide) {
             unit = (c & 32) >> 3;
+            if (p.out_dtype == 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float a = __uint_as_float(o[2 * e]), b = __uint_as_float(o[2 * e + 1]);
-                o[e] = p.out_dtype == 0 ? pack2<__half>(a, b) : pack2<__nv_bfloat16>(a, b);
+                for (int e = 0; e < 16; ++e) o[e] = pack2<__half>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    o[e] = pack2<__nv_bfloat16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
             }
         }
+        uint8_t* mine = stage + lane * 128;
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (u < 4 || wide)
-                *reinterpret_cast<uint4*>(stage + lane * 128 + (((unit + u) ^ (lane & 7)) << 4)) =
+        for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(mine + (((unit + u) ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        if (wide) {
+#pragma unroll
+            for (int u = 4; u < 8; ++u)
+                *reinterpret_cast<uint4*>(mine + ((u ^ (lane & 7)) << 4)) =
                     make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        }
         if (!wide && (c & 32) == 0) continue;
         __syncwarp();
 #pragma unroll
@@ -546,7 +562,7 @@ __device__ __forceinline__ float write_rows(const PromptParams& p, uint8_t* stag
         dst += 128;
         __syncwarp();
     }
-    return odd;
+    return odd.x + odd.y;
 }
 
 template <typename T>
@@ -913,7 +929,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const bool empty = seen <= j0 * kTile || !done;
-            const float inv = p.n_splits > 1 ? 1.f : 1.f / l;
+            // (an empty row's O is nothing: 1 keeps its zeros)
+            const float inv = p.n_splits > 1 || empty ? 1.f : __frcp_rn(l);
             const int rows = min(32, w.nq - w.pos[t] - 32 * (warp & 3));   // of this warp that exist
             const int64_t row0 = out_row(p, w, t, i - lane);
             const int64_t row_step = p.n_splits > 1 ? static_cast<int64_t>(p.n_q_heads) * p.n_splits : p.n_q_heads;
@@ -923,7 +940,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             __syncwarp();
             if (done && lane == 0) mbar_arrive(bar(kBarOF + t));
             if (real && p.n_splits == 1) {
-                if (p.lse != nullptr) p.lse[at0 + lane * row_step] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+                if (p.lse != nullptr) p.lse[at0 + lane * row_step] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
             } else if (real) {
                 p.ws_m[at0 + lane * row_step] = empty ? -INFINITY : m;
                 p.ws_l[at0 + lane * row_step] = empty ? 0.f : l;
