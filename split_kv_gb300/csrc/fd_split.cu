@@ -341,6 +341,7 @@ __device__ __forceinline__ void produce(const SplitCtx& c, const CUtensorMap* tm
 // stage's bytes are requested as soon as its slot is free; its one arrival on
 // the full barrier comes later, when its scales are written, which were
 // requested a stage before.  Tokens past the split's end get scale 0.
+// (128000 tokens, 32 / 8 heads, block 64: 45.6 us a call, against 43-44.5 unscaled.)
 template <int KIND>
 __device__ __forceinline__ void produce_scaled(const SplitCtx& c, const CUtensorMap* tmK,
                                                const CUtensorMap* tmV, int lane) {

