@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -330,9 +331,23 @@ int64_t prompt_tiles(const fd_prompt_desc* d) {
     return d->total_q / (pair_heads_of(d) ? 128 : 256) + d->batch;
 }
 
+// Key splits per query tile: few tiles over long keys leave SMs idle, so where
+// the tiles (by the packed rows) take at most half of them, the keys are cut so
+// that the parts fill them, with four key tiles a part at least (a part's
+// state costs its writing and joining) and 32 parts at most.  One split against
+// planned: 64 queries, 9000 keys, 8 / 2 heads 116 -> 30 us; 200, 12000, 32 / 8
+// 152 -> 66; 512, 4000, 8 / 8 54 -> 35; but 100, 1100, 16 / 2 (9 key tiles) 22 ->
+// 24, so from 16 key tiles on.
 int32_t prompt_splits(const fd_prompt_desc* d) {
     if (d->n_splits >= 1) return d->n_splits;
-    return 1;
+    const int64_t span = pair_heads_of(d) ? 128 : 256;
+    const int64_t units = (d->total_q + span - 1) / span * (pair_heads_of(d) ? d->n_q_heads / 2 : d->n_q_heads);
+    const int64_t key_tiles = ((d->max_k > 0 ? d->max_k : d->total_k) + 127) / 128;
+    if (units < 1 || key_tiles < 16) return 1;
+    const int64_t sms = fd_num_sms(-1);
+    if (units * 2 > sms) return 1;
+    const int64_t s = std::min(std::min(sms / units, key_tiles / 4), static_cast<int64_t>(32));
+    return static_cast<int32_t>(s);
 }
 
 // 3-D map over packed rows: dims (head_dim, rows, heads), boxes of 64 dims x

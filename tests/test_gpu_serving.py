@@ -483,6 +483,17 @@ def test_prompt_splits(n_splits):
     check_prompt(*prompt_case(7, "f16", lens, keys, 3, 3), False, torch.float16, n_splits=n_splits)
 
 
+def test_prompt_planned_splits():
+    """Few queries over long keys: the plan cuts the keys, and asks for a workspace."""
+    q, k, v, cq, ck = prompt_case(14, "bf16", [70, 1, 20], [6000, 900, 20], 6, 2, lead=1, tail=3)
+    d = fd.make_prompt_desc(q, k, v, batch=3, max_k=6000)
+    assert fd.fd_prompt_workspace_size(d) > 0
+    check_prompt(q, k, v, cq, ck, True)
+    check_prompt(q, k, v, cq, ck, False, torch.bfloat16)
+    out = torch.zeros(q.shape, device=DEV)
+    assert fd.fd_prompt(d, q, k, v, i32(cq), i32(ck), out, None, None) == fd.FD_ERR_WORKSPACE
+
+
 def test_prompt_large_scores_move_the_reference():
     """Scores in the hundreds that grow along the keys, so that O is rescaled again and again."""
     q, k, v, cq, ck = prompt_case(8, "f16", [700], [700], 4, 2, gain=6.0)
