@@ -118,7 +118,9 @@ typedef enum fd_dtype { FD_F16 = 0, FD_BF16 = 1, FD_F32 = 2, FD_E4M3 = 3 } fd_dt
  * v_* strides describe v_cache the same way.
  * Alignment (TMA): cache base addresses 16-byte aligned and every stride a
  * multiple of 16 bytes (8 elements of 16 bits, 16 of FD_E4M3); q rows
- * 16-byte aligned. */
+ * 16-byte aligned.  A cache's stride of 0 is allowed only over a dimension
+ * with one entry (sequences or KV heads that share their rows, as torch's
+ * expand makes them: FD_ERR_INVALID_ARG). */
 typedef struct fd_desc {
     int32_t batch;              /* B >= 0; B = 0 enqueues nothing */
     int32_t n_q_heads;          /* Hq >= 1 */
@@ -426,7 +428,8 @@ fd_status fd_page_tables(const fd_page_desc* desc, const int32_t* seqlens,
 /* Whole prompts: packed sequences of different lengths.
  * q   [total_q, n_q_heads, 128] at q + t*q_stride_t + h*q_stride_h, k and v
  * [total_k, n_kv_heads, 128] likewise (16-byte aligned bases, strides multiples
- * of 8 elements); rows cu_q[b] .. cu_q[b+1]-1 of q and cu_k[b] .. cu_k[b+1]-1 of k
+ * of 8 elements, a head stride of 0 only with one head: heads that share their
+ * rows are given as one KV head); rows cu_q[b] .. cu_q[b+1]-1 of q and cu_k[b] .. cu_k[b+1]-1 of k
  * and v belong to sequence b. */
 typedef struct fd_prompt_desc {
     int32_t batch;              /* sequences >= 0; 0 enqueues nothing */

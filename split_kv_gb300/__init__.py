@@ -468,7 +468,7 @@ def make_prompt_desc(q, k, v, *, batch: int, causal: bool = True, max_q: int = 0
                      n_splits: int = 0, out_dtype=None) -> FdPromptDesc:
     """Descriptor for packed prompts q [total_q, Hq, D], k and v [total_k, Hkv, D]
     (16-bit; any strides with a contiguous head dimension, so slices of one
-    projection's output too)."""
+    projection's output too, but no expanded heads: those are one KV head)."""
     import torch
     if not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k and v must have one type")

@@ -42,6 +42,10 @@ bool stride_ok(int64_t s, int esize = 2) {
     return s >= 0 && (s * esize) % 16 == 0 && s < (int64_t(1) << 38);
 }
 
+// A stride of 0 over several entries (rows shared, as by torch's expand): a
+// tensor map has none, whatever stride it was given instead would read other rows.
+bool shared_rows(int64_t stride, int64_t entries) { return stride == 0 && entries > 1; }
+
 int log2_of(int32_t x) {   // of a power of two
     int n = 0;
     while ((1 << n) < x) ++n;
@@ -171,7 +175,7 @@ fd_status make_map(CUtensorMap* map, const fd_desc* d, const void* base, int64_t
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(n_tok),
                           static_cast<cuuint64_t>(d->n_kv_heads), static_cast<cuuint64_t>(n_outer)};
     // byte strides of dims 1..3; a stride of a size-1 dim is never used, but
-    // must still be a valid multiple of 16
+    // must still be a valid multiple of 16 (other strides of 0 are refused)
     const int es = cache_esize(d);
     auto bs = [es](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s * es : 16); };
     cuuint64_t strides[3] = {bs(st), bs(sh), bs(sb)};
@@ -199,6 +203,10 @@ fd_status split_impl(const fd_desc* d, int32_t S, const void* q, const void* k, 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return FD_ERR_INVALID_ARG;
     const bool paged = d->page_size > 0;
     if (paged != (block_table != nullptr)) return FD_ERR_INVALID_ARG;
+    const int64_t outer = paged ? d->kv_extent : d->batch;
+    if (shared_rows(d->k_stride_b, outer) || shared_rows(d->v_stride_b, outer) ||
+        shared_rows(d->k_stride_h, d->n_kv_heads) || shared_rows(d->v_stride_h, d->n_kv_heads))
+        return FD_ERR_INVALID_ARG;
     const int64_t rows = rows_of(d);
     const WsLayout w = ws_layout(rows, S);
     if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return FD_ERR_WORKSPACE;
@@ -321,6 +329,9 @@ fd_status check_prompt(const fd_prompt_desc* d) {
     for (const int64_t s : {d->q_stride_t, d->q_stride_h, d->k_stride_t, d->k_stride_h, d->v_stride_t, d->v_stride_h})
         if (!stride_ok(s)) return FD_ERR_INVALID_ARG;
     if (d->q_stride_t < kHeadDim || d->k_stride_t < kHeadDim || d->v_stride_t < kHeadDim) return FD_ERR_INVALID_ARG;
+    if (shared_rows(d->q_stride_h, d->n_q_heads) || shared_rows(d->k_stride_h, d->n_kv_heads) ||
+        shared_rows(d->v_stride_h, d->n_kv_heads))
+        return FD_ERR_INVALID_ARG;
     return FD_OK;
 }
 
@@ -357,6 +368,7 @@ fd_status make_rows_map(CUtensorMap* map, bool bf16, const void* base, int64_t r
     if (enc == nullptr) return FD_ERR_CUDA;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(rows),
                           static_cast<cuuint64_t>(heads), 1};
+    // (a stride of 0 belongs to a size-1 dim here, see shared_rows)
     auto bs = [](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s * 2 : 16); };
     cuuint64_t strides[3] = {bs(st), bs(sh), 16};
     cuuint32_t box[4] = {64, 128, 1, 1};

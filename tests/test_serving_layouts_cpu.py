@@ -1,0 +1,57 @@
+"""Layouts that the kernels cannot address, refused on the host.  CPU only."""
+import pytest
+import torch
+
+from test_serving_cpu import _prompt, _scales, _store, fd  # noqa: F401
+
+
+def _decode(fd, **kw):
+    d = fd.FdDesc()
+    d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = 3, 32, 8, 128
+    d.kv_dtype = d.q_dtype = fd.FD_F16
+    d.q_stride_b, d.q_stride_h = 32 * 128, 128
+    d.k_stride_b = d.v_stride_b = 8 * 64 * 128
+    d.k_stride_h = d.v_stride_h = 64 * 128
+    d.k_stride_t = d.v_stride_t = 128
+    d.kv_extent, d.n_splits, d.k_scale, d.v_scale = 64, 2, 1.0, 1.0
+    for name, value in kw.items():
+        setattr(d, name, value)
+    return d
+
+
+@pytest.mark.parametrize("field", ["q_stride_h", "k_stride_h", "v_stride_h"])
+def test_prompt_refuses_heads_that_share_their_rows(fd, field):  # noqa: F811
+    """A head stride of 0 (torch's expand) has no tensor map; with one head it is never used."""
+    d = _prompt(fd)
+    setattr(d, field, 0)
+    assert fd.fd_prompt(d, 1024, 1024, 1024, 1024, 1024, 1024, None, None, 0, stream=0) == fd.FD_ERR_INVALID_ARG
+    assert fd.fd_prompt_workspace_size(d) == 0
+    d = _prompt(fd)
+    d.n_q_heads = d.n_kv_heads = 1
+    d.n_splits = 3
+    setattr(d, field, 0)
+    assert fd.fd_prompt_workspace_size(d) > 0
+
+
+def test_prompt_refuses_an_expanded_tensor(fd):  # noqa: F811
+    q, k = torch.zeros(4, 8, 128, dtype=torch.float16), torch.zeros(4, 1, 128, dtype=torch.float16)
+    d = fd.make_prompt_desc(q, k.expand(-1, 8, -1), k.expand(-1, 8, -1), batch=1)
+    assert fd.fd_prompt(d, 1024, 1024, 1024, 1024, 1024, 1024, None, None, 0, stream=0) == fd.FD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("field", ["k_stride_b", "k_stride_h", "v_stride_b", "v_stride_h"])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_refuses_a_cache_that_shares_its_rows(fd, field, paged, fp8):  # noqa: F811
+    kw = {field: 0}
+    if paged:
+        kw.update(page_size=64, max_pages_per_seq=4, kv_extent=9)
+    if fp8:
+        kw.update(kv_dtype=fd.FD_E4M3)
+    d = _decode(fd, **kw)
+    table = 1024 if paged else None
+    args = (1024, 1024, 1024, 1024, table, 1024, 1024, 1024, 1 << 30)
+    assert fd.fd_decode(d, *args, stream=0) == fd.FD_ERR_INVALID_ARG
+    assert fd.fd_split_states(d, 1024, 1024, 1024, 1024, table, 1024, 1 << 30, stream=0) == fd.FD_ERR_INVALID_ARG
+    if fp8:
+        assert fd.fd_decode_scaled(d, _scales(fd), *args, stream=0) == fd.FD_ERR_INVALID_ARG
