@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fdk {
 
 constexpr int kHeadDim = 128;     // D
@@ -133,6 +135,20 @@ int32_t plan_launch(int64_t batch, int64_t n_kv_heads, int cols, bool fp8, bool 
 // 0 when no context is current or the driver cannot say.  Per-context state
 // (the fixed workspace's address, kernel attributes) is keyed on it.
 unsigned long long current_context_id();
+
+// Raises the dynamic shared-memory limit of `kern` to `smem`, once per CUDA
+// context (the attribute belongs to the context's copy of the kernel).  With
+// no readable context id it is set on every launch; the call is idempotent.
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, size_t smem, std::atomic<unsigned long long>& configured_ctx) {
+    const unsigned long long ctx = current_context_id();
+    if (ctx != 0 && configured_ctx.load(std::memory_order_acquire) == ctx) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess && ctx != 0) configured_ctx.store(ctx, std::memory_order_release);
+    return e;
+}
+
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 
 // ---- page tables, store into a block-scaled cache, prompt attention

@@ -46,7 +46,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "../../include/fd.h"
@@ -1005,17 +1004,13 @@ cudaError_t launch_prompt_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, cons
                             const PromptParams& p, int64_t tiles, cudaStream_t stream) {
     auto kern = fd_prompt_kernel<T>;
     static std::atomic<unsigned long long> configured_ctx{0};
-    const unsigned long long ctx = current_context_id();
-    if (ctx == 0 || configured_ctx.load(std::memory_order_acquire) != ctx) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        if (ctx != 0) configured_ctx.store(ctx, std::memory_order_release);
-    }
+    cudaError_t e = allow_smem(kern, kSmem, configured_ctx);
+    if (e != cudaSuccess) return e;
     const int64_t units = tiles * p.head_units;
     const int64_t items = units * p.n_splits;
     const int sms = fd_num_sms(-1);
     if (sms < 1) return cudaErrorInvalidDevice;
-    cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kPromptThreads), kSmem,
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kPromptThreads), kSmem,
                                stream, tmQ, tmK, tmV, p);
     if (e != cudaSuccess || p.n_splits == 1) return e;
     return launch_pdl(fd_prompt_join_kernel, dim3(static_cast<unsigned>(units), 8), dim3(256), 0, stream, p);

@@ -2268,19 +2268,6 @@ __global__ void __launch_bounds__(Geo<KIND>::kThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Raises the dynamic shared-memory limit of `kern` to `smem`, once per CUDA
-// context (the attribute belongs to the context's copy of the kernel).  With
-// no readable context id it is set on every launch; the call is idempotent.
-template <typename Kern>
-static cudaError_t allow_smem(Kern kern, size_t smem, std::atomic<unsigned long long>& configured_ctx) {
-    const unsigned long long ctx = current_context_id();
-    if (ctx != 0 && configured_ctx.load(std::memory_order_acquire) == ctx) return cudaSuccess;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess && ctx != 0) configured_ctx.store(ctx, std::memory_order_release);
-    return e;
-}
-
 template <typename T, int KIND>
 static cudaError_t launch_split_t(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                   const SplitParams& p, int batch, int n_kv_heads,

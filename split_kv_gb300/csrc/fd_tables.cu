@@ -13,6 +13,7 @@
 // token's sequence by bisection in shared memory.  The outputs that may alias
 // inputs are written behind a cluster barrier, after every CTA has read them.
 // 64 requests of one token: 3.1 us; 60000 tokens of 8 requests: 10.5 us.
+#include "../../include/fd.h"
 #include "fd_device.cuh"
 #include "fd_internal.h"
 
@@ -166,11 +167,12 @@ cudaError_t launch_page_tables(const PageParams& p, cudaStream_t stream) {
     const int ctas = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
     const int threads = p.n_slots <= 256 && p.batch <= 256 ? 256 : 1024;
     const size_t smem = (3 * static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fd_page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    // the limit of the largest batch, whatever this call's is (the default of
+    // 48 KB counts the static arrays too): calls of two threads never lower it
+    // under each other
+    static std::atomic<unsigned long long> configured_ctx{0};
+    cudaError_t e = allow_smem(fd_page_tables_kernel, (3 * FD_MAX_TABLE_BATCH + 1) * sizeof(int32_t), configured_ctx);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
@@ -185,7 +187,7 @@ cudaError_t launch_page_tables(const PageParams& p, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fd_page_tables_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, fd_page_tables_kernel, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

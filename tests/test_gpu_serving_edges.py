@@ -1,0 +1,61 @@
+"""The serving operators at the edges of what their calls allow: batches around
+the shared-memory limit, empty steps, many infinities, several threads."""
+import os
+import subprocess
+import sys
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import serving_ref as ref
+import split_kv_gb300 as fd
+from test_gpu_serving import (DEV, NAN, D, _clean_status, _lib, cumulative, gen, i32, prompt_case, randn,  # noqa: F401
+                              run_prompt, run_tables, table_case)
+
+pytestmark = pytest.mark.gpu
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+# ------------------------------------------------------------------ page tables
+def check_tables(batch, page=16, width=4, top_new=2):
+    case = table_case(batch, batch, page, width, top_new)
+    lens, new, free, count, table, n_pages, n_slots = case
+    want = ref.tables(lens, new, free, count, table, page, n_pages, n_slots)
+    got = run_tables(lens, new, free, count, table, page, n_pages, n_slots)
+    for name, a, b in zip(("lens", "count", "table", "cu", "slots", "positions"), got, want):
+        assert a == b, (batch, name)
+
+
+def test_tables_around_the_default_shared_memory_limit():
+    """3 * 4 batch + 4 bytes of dynamic and 272 of static shared memory pass 48 KB
+    from batch 4074 on.  A process of its own: no larger batch has been there before."""
+    code = ("import sys; sys.path.insert(0, %r); sys.path.insert(0, %r); import torch, test_gpu_serving_edges as t\n"
+            "for b in (4073, 4074, 4095, 4096, 8192): t.check_tables(b)\n"
+            "assert t.fd.fd_device_status() == 0; print('fine')" % (HERE, os.path.dirname(HERE)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_tables_of_two_threads_with_batches_of_different_sizes():
+    cases = {b: table_case(b, b, 16, 4, 2) for b in (4200, 8000)}
+    want = {b: ref.tables(*c[:5], 16, c[5], c[6]) for b, c in cases.items()}
+    failed = []
+
+    def work(b):
+        lens, new, free, count, table, n_pages, n_slots = cases[b]
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = run_tables(lens, new, free, count, table, 16, n_pages, n_slots)
+                    assert all(x == y for x, y in zip(got, want[b]))
+        except Exception as e:                     # a thread's failure is the test's
+            failed.append(f"{b}: {e!r}"[:500])
+
+    threads = [threading.Thread(target=work, args=(b,)) for b in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
