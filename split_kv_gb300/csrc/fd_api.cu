@@ -570,12 +570,12 @@ fd_status fd_cache_store(const fd_store_desc* d, const fd_kv_scales* scales, con
     const fd_status st = check_scales(scales, d->page_size);
     if (st != FD_OK) return st;
     if (d->n_kv_heads > 65535) return FD_ERR_UNSUPPORTED;
+    if (d->n_tokens == 0) return FD_OK;   // (an empty tensor's address is null)
     if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr || v_cache == nullptr)
         return FD_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
         (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
         return FD_ERR_INVALID_ARG;
-    if (d->n_tokens == 0) return FD_OK;
     fdk::StoreParams p;
     p.side[0] = {k, static_cast<uint8_t*>(k_cache), scales->k, d->k_src_stride_t, d->k_src_stride_h,
                  d->k_stride_b, d->k_stride_h, d->k_stride_t, scales->k_stride_b, scales->k_stride_h, scales->k_stride_n};

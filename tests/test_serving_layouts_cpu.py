@@ -55,3 +55,19 @@ def test_decode_refuses_a_cache_that_shares_its_rows(fd, field, paged, fp8):  # 
     assert fd.fd_split_states(d, 1024, 1024, 1024, 1024, table, 1024, 1 << 30, stream=0) == fd.FD_ERR_INVALID_ARG
     if fp8:
         assert fd.fd_decode_scaled(d, _scales(fd), *args, stream=0) == fd.FD_ERR_INVALID_ARG
+
+
+def test_store_of_no_rows_takes_empty_tensors(fd):  # noqa: F811
+    """A step without new rows: the address of an empty tensor is null."""
+    d = _store(fd)
+    d.n_tokens = 0
+    for k, v, slots, kc, vc in ((None, None, None, 1024, 1024), (1024, 1024, None, 1024, 1024), (None,) * 5):
+        assert fd.fd_cache_store(d, _scales(fd), k, v, slots, kc, vc, stream=0) == fd.FD_OK
+    d.n_tokens = 1
+    assert fd.fd_cache_store(d, _scales(fd), 1024, 1024, None, 1024, 1024, stream=0) == fd.FD_ERR_INVALID_ARG
+    none = torch.empty(0, 2, 128, dtype=torch.float16)
+    kc, vc = (torch.zeros(10, 2, 64, 128).to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = torch.ones(10, 2, 4), torch.ones(10, 2, 4)
+    d = fd.make_store_desc(none, none, kc, vc, page_size=64)
+    slots = torch.empty(0, dtype=torch.int64)
+    assert fd.fd_cache_store(d, fd.make_scales(ks, vs, block=16), none, none, slots, kc, vc, stream=0) == fd.FD_OK
