@@ -510,6 +510,7 @@ fd_status fd_decode_scaled(const fd_desc* desc, const fd_kv_scales* scales, cons
     if (!is_fp8(desc)) return FD_ERR_INVALID_ARG;
     st = check_scales(scales, desc->page_size);
     if (st != FD_OK) return st;
+    if (desc->batch == 0) return FD_OK;   // (an empty tensor's address is null)
     if (out == nullptr) return FD_ERR_INVALID_ARG;
     const int32_t S = splits_for(desc);
     if (S < 1) return static_cast<fd_status>(S < 0 ? S : FD_ERR_INVALID_ARG);

@@ -71,3 +71,11 @@ def test_store_of_no_rows_takes_empty_tensors(fd):  # noqa: F811
     d = fd.make_store_desc(none, none, kc, vc, page_size=64)
     slots = torch.empty(0, dtype=torch.int64)
     assert fd.fd_cache_store(d, fd.make_scales(ks, vs, block=16), none, none, slots, kc, vc, stream=0) == fd.FD_OK
+
+
+def test_scaled_decode_of_no_sequences_takes_empty_tensors(fd):  # noqa: F811
+    d = _decode(fd, batch=0, kv_dtype=fd.FD_E4M3, page_size=64, max_pages_per_seq=4)
+    assert fd.fd_decode_scaled(d, _scales(fd), None, 1024, 1024, None, None, None, None, None, 0, stream=0) == fd.FD_OK
+    d.batch = 1
+    assert fd.fd_decode_scaled(d, _scales(fd), None, 1024, 1024, 1024, 1024, 1024, None, 1024, 1 << 30,
+                               stream=0) == fd.FD_ERR_INVALID_ARG
