@@ -321,7 +321,9 @@ fd_status fd_decode_static(const fd_desc* desc, const void* q, const void* k_cac
  *     stored * k[P*k_stride_b + g*k_stride_h + (t / block)*k_stride_n]
  * with t counted within the page (paged) or the sequence (contiguous).
  * Strides in elements, >= 0.  fd_decode_scaled reads any non-negative finite
- * scales; fd_cache_store writes powers of two.
+ * scales, several blocks' in one place (a stride of 0) too; fd_cache_store
+ * writes powers of two, each block's in a place of its own (a stride of 0 of
+ * the scales or the cache over several entries: FD_ERR_INVALID_ARG).
  * block: a power of two, 1 <= block <= 1024; paged: at most page_size. */
 typedef struct fd_kv_scales {
     float* k;                   /* device */

@@ -571,6 +571,15 @@ fd_status fd_cache_store(const fd_store_desc* d, const fd_kv_scales* scales, con
     const fd_status st = check_scales(scales, d->page_size);
     if (st != FD_OK) return st;
     if (d->n_kv_heads > 65535) return FD_ERR_UNSUPPORTED;
+    // what is written has a place of its own
+    const int64_t lead = d->page_size > 0 ? d->kv_extent : d->batch;
+    const int64_t blocks = ((d->page_size > 0 ? d->page_size : d->kv_extent) + scales->block - 1) / scales->block;
+    if (shared_rows(d->k_stride_b, lead) || shared_rows(d->v_stride_b, lead) ||
+        shared_rows(d->k_stride_h, d->n_kv_heads) || shared_rows(d->v_stride_h, d->n_kv_heads) ||
+        shared_rows(scales->k_stride_b, lead) || shared_rows(scales->v_stride_b, lead) ||
+        shared_rows(scales->k_stride_h, d->n_kv_heads) || shared_rows(scales->v_stride_h, d->n_kv_heads) ||
+        shared_rows(scales->k_stride_n, blocks) || shared_rows(scales->v_stride_n, blocks))
+        return FD_ERR_INVALID_ARG;
     if (d->n_tokens == 0) return FD_OK;   // (an empty tensor's address is null)
     if (k == nullptr || v == nullptr || slots == nullptr || k_cache == nullptr || v_cache == nullptr)
         return FD_ERR_INVALID_ARG;

@@ -79,3 +79,25 @@ def test_scaled_decode_of_no_sequences_takes_empty_tensors(fd):  # noqa: F811
     d.batch = 1
     assert fd.fd_decode_scaled(d, _scales(fd), None, 1024, 1024, 1024, 1024, 1024, None, 1024, 1 << 30,
                                stream=0) == fd.FD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("field", ["k_stride_b", "k_stride_h", "v_stride_b", "v_stride_h"])
+def test_store_refuses_a_cache_that_shares_its_rows(fd, field, paged):  # noqa: F811
+    """Rows of two pages or heads in one place: which of them it keeps would be chance."""
+    d = _store(fd)
+    if not paged:
+        d.page_size, d.kv_extent, d.batch = 0, 64, 5
+    setattr(d, field, 0)
+    assert fd.fd_cache_store(d, _scales(fd), 1024, 1024, 1024, 1024, 1024, stream=0) == fd.FD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("field", ["k_stride_b", "k_stride_h", "k_stride_n", "v_stride_b", "v_stride_h", "v_stride_n"])
+def test_store_refuses_scales_that_several_blocks_share(fd, field, paged):  # noqa: F811
+    """The decode may read one scale for many blocks, the store writes each block's own."""
+    d, s = _store(fd), _scales(fd)
+    if not paged:
+        d.page_size, d.kv_extent, d.batch = 0, 64, 5
+    setattr(s, field, 0)
+    assert fd.fd_cache_store(d, s, 1024, 1024, 1024, 1024, 1024, stream=0) == fd.FD_ERR_INVALID_ARG
