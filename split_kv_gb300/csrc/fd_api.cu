@@ -739,9 +739,6 @@ fd_status fd_device_status(void* stream, int32_t clear) {
     unsigned v = 0;
     if (fdk::read_status(&v, static_cast<cudaStream_t>(stream), clear != 0) != cudaSuccess)
         return FD_ERR_CUDA;
-    if (fdk::status_tables(&v, clear != 0) != cudaSuccess || fdk::status_store(&v, clear != 0) != cudaSuccess ||
-        fdk::status_prompt(&v, clear != 0) != cudaSuccess)
-        return FD_ERR_CUDA;
     if (v & fdk::kStatusTimeoutBit) return FD_ERR_DEVICE_TIMEOUT;
     if (v != 0) return FD_ERR_DEVICE_BOUNDS;
     return FD_OK;

@@ -207,26 +207,14 @@ struct PromptParams {
 // tiles: query tiles (of 128 positions, or 256) that the sequences can have at most.
 cudaError_t launch_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           const PromptParams& p, bool bf16, int64_t tiles, cudaStream_t stream);
-cudaError_t status_prompt(unsigned* value, bool clear);
 
-// Each file that raises status bits owns a word; fd_device_status joins them.
-// Called with the stream already synchronised.
-#ifdef __CUDACC__
-inline cudaError_t read_status_word(unsigned& symbol, unsigned* value, bool clear) {
-    unsigned v = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, symbol, sizeof(unsigned));
-    if (e == cudaSuccess && clear && v != 0) {
-        const unsigned zero = 0;
-        e = cudaMemcpyToSymbol(symbol, &zero, sizeof(unsigned));
-    }
-    *value |= v;
-    return e;
-}
-#endif
-cudaError_t status_tables(unsigned* value, bool clear);
-cudaError_t status_store(unsigned* value, bool clear);
+// The status words.  Each file that raises bits owns one (device symbols do
+// not cross files here); read_status joins them.
+cudaError_t status_word_tables(unsigned** word);
+cudaError_t status_word_store(unsigned** word);
+cudaError_t status_word_prompt(unsigned** word);
 
-// Device status word helpers (fd_split.cu owns the symbol).
+// Waits for `stream`, then reads (and with `clear` resets) every status word (fd_split.cu).
 cudaError_t read_status(unsigned* value, cudaStream_t stream, bool clear);
 
 }  // namespace fdk

@@ -1024,6 +1024,8 @@ cudaError_t launch_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const 
                 : launch_prompt_t<__half>(tmQ, tmK, tmV, p, tiles, stream);
 }
 
-cudaError_t status_prompt(unsigned* value, bool clear) { return read_status_word(g_status, value, clear); }
+cudaError_t status_word_prompt(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_status);
+}
 
 }  // namespace fdk

@@ -371,6 +371,8 @@ cudaError_t launch_store(const StoreParams& p, bool bf16, cudaStream_t stream) {
     return bf16 ? launch_store_t<__nv_bfloat16>(p, stream) : launch_store_t<__half>(p, stream);
 }
 
-cudaError_t status_store(unsigned* value, bool clear) { return read_status_word(g_status, value, clear); }
+cudaError_t status_word_store(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_status);
+}
 
 }  // namespace fdk

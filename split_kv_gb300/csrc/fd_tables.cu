@@ -191,6 +191,8 @@ cudaError_t launch_page_tables(const PageParams& p, cudaStream_t stream) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t status_tables(unsigned* value, bool clear) { return read_status_word(g_status, value, clear); }
+cudaError_t status_word_tables(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_status);
+}
 
 }  // namespace fdk

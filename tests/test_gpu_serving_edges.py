@@ -59,3 +59,24 @@ def test_tables_of_two_threads_with_batches_of_different_sizes():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+# ------------------------------------------------------------------ the status word
+def test_status_keeps_bits_of_every_operator_until_cleared():
+    """Bits that the page tables, the store and the prompt attention raised are joined, and stay where a read does not clear."""
+    lens, new, free, count, table, n_pages, n_slots = table_case(3, 4, 16, 8, 20)
+    k = randn(gen(1), "f16", 1, 2, D)
+    cache = [torch.zeros(3, 2, 16, D, device=DEV).to(ref.F8) for _ in range(2)]
+    scales = [torch.ones(3, 2, 1, device=DEV) for _ in range(2)]
+    q, pk, pv, cq, ck = prompt_case(1, "f16", [20], [20], 2, 1)
+    raisers = (lambda: run_tables(lens, new, free, len(free) + 1, table, 16, n_pages, n_slots),
+               lambda: fd.check(fd.fd_cache_store(fd.make_store_desc(k, k, *cache, page_size=16), fd.make_scales(*scales, block=16),
+                                                  k, k, torch.tensor([48], device=DEV), *cache)),
+               lambda: run_prompt(q, pk, pv, cq, [0, 21], True))
+    for some in ((0,), (1,), (2,), (0, 1, 2)):
+        for i in some:
+            raisers[i]()
+        for _ in range(2):
+            assert fd.fd_device_status(clear=False) == fd.FD_ERR_DEVICE_BOUNDS
+        assert fd.fd_device_status(clear=True) == fd.FD_ERR_DEVICE_BOUNDS
+        assert fd.fd_device_status(clear=True) == fd.FD_OK
