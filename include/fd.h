@@ -462,7 +462,9 @@ size_t fd_prompt_workspace_size(const fd_prompt_desc* desc);
  * causal: the queries are the last nq of the nk positions, query i sees keys
  * j <= i + nk - nq (a prompt's chunk behind keys that are there already has nk >
  * nq).  A query that sees no key gets out = 0 and lse = -inf.
- * A key's or value's infinities and NaN reach only the queries that see it.
+ * A key's or value's infinities and NaN reach only the queries that see it
+ * (rows that share a tile of 128 with such a value of V behind their last key
+ * are computed a second time, slowly).
  *  cu_q, cu_k : device int32[batch+1], ascending, within [0, total_q] and
  *               [0, total_k].  A sequence for which that does not hold is skipped
  *               and sets FD_ERR_DEVICE_BOUNDS in the status word.

@@ -37,8 +37,8 @@
 // is NaN: V's rows past the sequence's end are zeroed in shared memory in the
 // one tile that has some (warp 10), and a row of O that comes out with an
 // infinity or NaN is looked into: if a key that the row does not see but whose
-// tile it walked has one in V, the row is computed again by a plain loop over
-// the keys that it sees.
+// tile it walked has one in V, and the row is not NaN by right, it is computed
+// again by a plain loop over the keys that it sees, once the CTA's items are done.
 //
 // Bound by the tensor cores when sequences are long: 4 * 128 flops per visible
 // pair and head against 2 bytes per element read once.  16384 tokens, 32 / 8
@@ -69,7 +69,7 @@ constexpr int kOffStage = kOffRing + kSlots * kSlotBytes;   // the epilogue's, 4
 constexpr int kOffBar = kOffStage + 8 * 4096;
 constexpr int kOffWork = kOffBar + 384; // [kWorks] Work, 64 bytes each
 constexpr int kWorks = 4;
-constexpr int kOffMisc = kOffWork + kWorks * 64;    // tensor memory address, abort flag
+constexpr int kOffMisc = kOffWork + kWorks * 64;    // tensor memory address, abort flag, redo flags
 constexpr int kSorted = 128;            // batches up to this are handed out largest first
 constexpr int kSmem = kOffMisc + 32 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
@@ -375,46 +375,103 @@ __device__ __forceinline__ void put_out4(const PromptParams& p, int64_t row, int
     }
 }
 
-// A row again, by one warp over the keys [j0, j1): lane l holds dims 4l .. 4l + 3.
+// Up to four rows again, by one warp, each over the keys that it sees in the
+// item's key tiles (lim: one past the last; at most j0: no such row): lane l
+// holds dims 4l .. 4l + 3.  Four keys at a time, so that their products and
+// the exchanges that add them up run beside each other.
 template <typename T>
-__device__ __noinline__ void plain_row(const PromptParams& p, const Work& w, int t, int i, int lane) {
-    const int j0 = w.j0 * kTile, j1 = min(w.j1 * kTile, seen_by(p, w.nq, w.nk, i));
-    const int g = w.head[t] / p.group;
-    const T* q = static_cast<const T*>(p.q) + (static_cast<int64_t>(w.q0) + i) * p.q_st + w.head[t] * p.q_sh + 4 * lane;
-    const uint2 qw = *reinterpret_cast<const uint2*>(q);
-    const float2 qa = unpack2<T>(qw.x), qb = unpack2<T>(qw.y);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = j0; j < j1; ++j) {
-        const int64_t row = static_cast<int64_t>(w.k0) + j;
-        const uint2 kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.k) + row * p.k_st + g * p.k_sh + 4 * lane);
-        const uint2 vw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v) + row * p.v_st + g * p.v_sh + 4 * lane);
-        const float2 ka = unpack2<T>(kw.x), kb = unpack2<T>(kw.y), va = unpack2<T>(vw.x), vb = unpack2<T>(vw.y);
-        float s = fmaf(qa.x, ka.x, fmaf(qa.y, ka.y, fmaf(qb.x, kb.x, qb.y * kb.y)));
+__device__ __noinline__ void plain_rows(const PromptParams& p, const Work& w, int t, const int (&row)[4], int lane) {
+    const int j0 = w.j0 * kTile, g = w.head[t] / p.group;
+    const T* kp = static_cast<const T*>(p.k) + static_cast<int64_t>(w.k0) * p.k_st + g * p.k_sh + 4 * lane;
+    const T* vp = static_cast<const T*>(p.v) + static_cast<int64_t>(w.k0) * p.v_st + g * p.v_sh + 4 * lane;
+    float q[4][4], o[4][4], m[4], l[4];
+    int lim[4], most = j0;
 #pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(kFullMask, s, x);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
-        const float a = fast_exp2(m - mu), e = fast_exp2(s - mu);
-        m = mn;
-        l = fmaf(l, a, e);
-        o[0] = fmaf(o[0], a, e * va.x);
-        o[1] = fmaf(o[1], a, e * va.y);
-        o[2] = fmaf(o[2], a, e * vb.x);
-        o[3] = fmaf(o[3], a, e * vb.y);
+    for (int r = 0; r < 4; ++r) {
+        lim[r] = row[r] >= 0 ? min(w.j1 * kTile, seen_by(p, w.nq, w.nk, row[r])) : 0;
+        most = max(most, lim[r]);
+        uint2 qw = make_uint2(0u, 0u);
+        if (row[r] >= 0)
+            qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + (static_cast<int64_t>(w.q0) + row[r]) * p.q_st +
+                                                 w.head[t] * p.q_sh + 4 * lane);
+        const float2 a = unpack2<T>(qw.x), b = unpack2<T>(qw.y);
+        q[r][0] = a.x, q[r][1] = a.y, q[r][2] = b.x, q[r][3] = b.y;
+        o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
     }
-    const int64_t row = out_row(p, w, t, i);
-    const bool empty = j1 <= j0;
-    if (p.n_splits == 1) {
+    uint2 kw[4], vw[4];                            // four keys ahead
+    auto load = [&](int j) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = empty ? 0.f : o[e] / l;
-        put_out4(p, row, 4 * lane, o);
-        if (lane == 0 && p.lse != nullptr) p.lse[row] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
-    } else {
-        const int64_t at = row * p.n_splits + w.split;
-        *reinterpret_cast<float4*>(p.ws_u + at * kHeadDim + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
-        if (lane == 0) {
-            p.ws_m[at] = m;
-            p.ws_l[at] = l;
+        for (int x = 0; x < 4; ++x) {
+            kw[x] = vw[x] = make_uint2(0u, 0u);
+            if (j + x < most) {
+                kw[x] = *reinterpret_cast<const uint2*>(kp + (j + x) * p.k_st);
+                vw[x] = *reinterpret_cast<const uint2*>(vp + (j + x) * p.v_st);
+            }
+        }
+    };
+    load(j0);
+#pragma unroll 1
+    for (int j = j0; j < most; j += 4) {
+        float k[4][4], v[4][4], s[4][4];           // [key], [key], [key][row]
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float2 ka = unpack2<T>(kw[x].x), kb = unpack2<T>(kw[x].y), va = unpack2<T>(vw[x].x), vb = unpack2<T>(vw[x].y);
+            k[x][0] = ka.x, k[x][1] = ka.y, k[x][2] = kb.x, k[x][3] = kb.y;
+            v[x][0] = va.x, v[x][1] = va.y, v[x][2] = vb.x, v[x][3] = vb.y;
+        }
+        load(j + 4);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                s[x][r] = fmaf(q[r][0], k[x][0], fmaf(q[r][1], k[x][1], fmaf(q[r][2], k[x][2], q[r][3] * k[x][3])));
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[x][r] += __shfl_xor_sync(kFullMask, s[x][r], d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float mn = m[r];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                s[x][r] = j + x < lim[r] ? s[x][r] * p.scale_log2 : -INFINITY;
+                mn = fmaxf(mn, s[x][r]);
+            }
+            const float mu = mn == -INFINITY ? 0.f : mn, a = fast_exp2(m[r] - mu);
+            m[r] = mn;
+            l[r] *= a;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][e] *= a;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (j + x < lim[r]) {              // (the same for the whole warp)
+                    const float e = fast_exp2(s[x][r] - mu);
+                    l[r] += e;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) o[r][d] = fmaf(e, v[x][d], o[r][d]);
+                }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (lim[r] <= j0) continue;
+        const int64_t to = out_row(p, w, t, row[r]);
+        if (p.n_splits == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][e] /= l[r];
+            put_out4(p, to, 4 * lane, o[r]);
+            if (lane == 0 && p.lse != nullptr) p.lse[to] = (m[r] + __log2f(l[r])) * kLn2;
+        } else {
+            const int64_t at = to * p.n_splits + w.split;
+            *reinterpret_cast<float4*>(p.ws_u + at * kHeadDim + 4 * lane) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+            if (lane == 0) {
+                p.ws_m[at] = m[r];
+                p.ws_l[at] = l[r];
+            }
         }
     }
 }
@@ -474,6 +531,98 @@ __device__ __noinline__ bool hidden_special(const PromptParams& p, const Work& w
         bad |= any_special<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + (static_cast<int64_t>(w.k0) + j) * p.v_st +
                                                               g * p.v_sh + 8 * (lane & 15)));
     return __any_sync(kFullMask, bad);
+}
+
+// Rank of the k-th item of this CTA: back and forth over the CTAs.
+__device__ __forceinline__ uint32_t item_rank(int k) {
+    return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// One item's rows of one warp (32 of query tile t, from 32 * quarter on) that an
+// infinity or NaN of V reached which they do not see.  Lane l looks through
+// dims 4l .. 4l + 3 for the last special value of the key tiles that some row
+// does not see whole, and for the key from which on a row's result is NaN by
+// right: the first NaN, or the later of the first +inf and -inf.  A row is
+// computed again if a dim of it has the one hidden and not yet the other; so
+// where V is NaN throughout hardly any is, and a first NaN in the middle costs
+// the rows of one tile.
+template <typename T>
+__device__ __noinline__ void redo_item(const PromptParams& p, const Work& w, int t, int quarter, int lane) {
+    constexpr uint32_t inf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    const int from = w.j0 * kTile;
+    const int first = max(from, seen_by(p, w.nq, w.nk, w.pos[t]) / kTile * kTile), last = min(w.n[t] * kTile, w.nk);
+    const T* vp = static_cast<const T*>(p.v) + static_cast<int64_t>(w.k0) * p.v_st + w.head[t] / p.group * p.v_sh + 4 * lane;
+    int nan_at[4], up_at[4], down_at[4], hidden[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        nan_at[d] = up_at[d] = down_at[d] = INT32_MAX;
+        hidden[d] = -1;
+    }
+    auto look = [&](int j, const uint2& vw, bool masked) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t x = ((d < 2 ? vw.x : vw.y) >> (16 * (d & 1))) & 0xffffu, a = x & 0x7fffu;
+            if (a < inf) continue;
+            if (masked) hidden[d] = max(hidden[d], j);
+            if (a > inf) nan_at[d] = min(nan_at[d], j);
+            else if (x == a) up_at[d] = min(up_at[d], j);
+            else down_at[d] = min(down_at[d], j);
+        }
+    };
+    auto nan_from = [&](int d) { return min(nan_at[d], max(up_at[d], down_at[d])); };
+#pragma unroll 4
+    for (int j = first; j < last; ++j) look(j, *reinterpret_cast<const uint2*>(vp + j * p.v_st), true);
+#pragma unroll 1
+    for (int j = from; j < first; j += 8) {          // (whole tiles)
+        bool known = true;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) known = known && (hidden[d] < 0 || nan_from(d) < first);
+        if (__all_sync(kFullMask, known)) break;
+        uint2 vw[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) vw[x] = *reinterpret_cast<const uint2*>(vp + (j + x) * p.v_st);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) look(j + x, vw[x], false);
+    }
+    int row[4], rows = 0;
+    const int i0 = w.pos[t] + 32 * quarter;
+#pragma unroll 1
+    for (int i = i0; i < i0 + 32; ++i) {
+        bool reached = false;
+        if (i < w.nq) {
+            const int seen = seen_by(p, w.nq, w.nk, i);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) reached = reached || (seen > from && hidden[d] >= seen && nan_from(d) >= seen);
+        }
+        const bool again = __any_sync(kFullMask, reached);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (again && x == rows) row[x] = i;
+        rows += again;
+        if (rows == 4 || (rows > 0 && i == i0 + 31)) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (x >= rows) row[x] = -1;
+            plain_rows<T>(p, w, t, row, lane);
+            rows = 0;
+        }
+    }
+}
+
+// All items of the CTA again, for such rows.  Runs when they are done: nothing
+// waits for this warp but the CTA's end, however long its rows take.  16384
+// tokens, 32 / 8 heads: 17 ms with one NaN in the middle of one KV head, 2.2
+// with NaN throughout, 254 with +inf throughout (every row again), 1.3 without.
+template <typename T>
+__device__ __noinline__ void redo_rows(const PromptParams& p, int t, int quarter, int lane) {
+    Dealer dealer;
+    dealer.start(p, lane, false);
+    for (int k = 0;; ++k) {
+        Work w;
+        dealer.item(p, item_rank(k), lane, w);
+        if (w.b < 0) break;
+        if (w.n[t] > w.j0 && hidden_special<T>(p, w, t, lane)) redo_item<T>(p, w, t, quarter, lane);
+    }
 }
 
 // 16 bytes of output at an address that has only its element's alignment
@@ -585,6 +734,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                               : i >= kBarWE && i < kBarWE + kWorks                             ? 11
                                                                                                : 1);
         *abort_flag = 0;
+        *reinterpret_cast<volatile uint64_t*>(smem + kOffMisc + 8) = 0;   // the softmax warps' flags to redo rows
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmK);
@@ -834,9 +984,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (k >= kWorks) ok = wait_bar_warp(bar(kBarWE + k % kWorks), (k / kWorks - 1) & 1, abort_flag);
                 if (!ok) break;
                 Work w;
-                // back and forth over the CTAs
-                const uint32_t at = k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-                dealer.item(p, k * gridDim.x + at, lane, w);
+                dealer.item(p, item_rank(k), lane, w);
                 if (lane == 0) {
                     *work_at(k) = w;
                     mbar_arrive(bar(kBarWF + k % kWorks));
@@ -854,6 +1002,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * t, to = tmem + lanes + 256u + 128u * t;
         const float sc = p.scale_log2;
+        volatile uint8_t* redo = smem + kOffMisc + 8 + warp;   // (a register less in the loop)
         uint32_t walked = 0, ran = 0;            // key tiles, and items with any: parities of S and O
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -945,16 +1094,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 p.ws_m[at0 + lane * row_step] = empty ? -INFINITY : m;
                 p.ws_l[at0 + lane * row_step] = empty ? 0.f : l;
             }
-            // rows that a value they do not see may have reached
-            unsigned again = __ballot_sync(kFullMask, real && odd != odd);
-            if (again != 0 && hidden_special<T>(p, w, t, lane)) {
-                __syncwarp();
-                for (; again != 0; again &= again - 1)
-                    plain_row<T>(p, w, t, w.pos[t] + 32 * (warp & 3) + __ffs(again) - 1, lane);
-            }
+            // rows that a value they do not see may have reached: done again at the
+            // end, so that no wait of the other roles depends on how long that takes
+            if (__any_sync(kFullMask, real && odd != odd) && hidden_special<T>(p, w, t, lane)) *redo = 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarWE + k % kWorks));
         }
+        __syncwarp();
+        if (ok && *redo) redo_rows<T>(p, t, warp & 3, lane);
         tc_fence_before();
     }
     __syncthreads();

@@ -80,3 +80,49 @@ def test_status_keeps_bits_of_every_operator_until_cleared():
             assert fd.fd_device_status(clear=False) == fd.FD_ERR_DEVICE_BOUNDS
         assert fd.fd_device_status(clear=True) == fd.FD_ERR_DEVICE_BOUNDS
         assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+# ------------------------------------------------------------------ prompts with many infinities
+@pytest.mark.parametrize("n_splits", [1, 3])
+@pytest.mark.parametrize("where,value", [("third", NAN), ("late", NAN), ("all", NAN), ("all", float("inf")),
+                                         ("dims", -float("inf")), ("mixed", None)])
+def test_prompt_many_special_values(where, value, n_splits):
+    """A few thousand keys of which many have infinities or NaN in V: results as
+    the definition's, and no wait of the kernel runs out however many rows are
+    computed again.  (bf16: no weight of these scores rounds to 0, so that an
+    infinity times its weight stays one.)"""
+    n = 3000 if where != "dims" else 2200
+    q, k, v, cq, ck = prompt_case(31, "bf16", [n, 200], [n + 70, 200], 4, 2)
+    if where == "third":
+        v[1000::3] = value
+    elif where == "late":
+        v[n // 2 + 5:, :, ::2] = value
+    elif where == "all":
+        v[:] = value
+    elif where == "dims":                          # another first one in every dim
+        for d in range(D):
+            v[17 * d + 11, :, d] = value
+    else:
+        g = gen(32)
+        at = torch.randint(0, v.numel(), (400,), generator=g, device=DEV)
+        kinds = torch.tensor([NAN, float("inf"), -float("inf")], device=DEV, dtype=v.dtype)
+        v.view(-1)[at] = kinds[torch.randint(0, 3, (400,), generator=g, device=DEV)]
+    out, lse = run_prompt(q, k, v, cq, ck, True, n_splits=n_splits)
+    clean = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+    o, z, tol, ltol = ref.prompt(q, k, clean, cq, ck, True, torch.float32)
+    ref.close(lse, z, ltol, "lse")
+    # which results are NaN or infinite by right: what kinds of values each row sees in each dim
+    for b in range(2):
+        nq, nk = cq[b + 1] - cq[b], ck[b + 1] - ck[b]
+        seen = torch.arange(nq, device=DEV) + nk - nq
+        for h in range(4):
+            vv, got = v[ck[b]:ck[b + 1], h // 2], out[cq[b]:cq[b + 1], h].double()
+            some = [x.cummax(0).values[seen] for x in (torch.isnan(vv).byte(), (vv == float("inf")).byte(), (vv == -float("inf")).byte())]
+            nan = (some[0] | (some[1] & some[2])).bool()
+            up, down = some[1].bool() & ~nan, some[2].bool() & ~nan
+            assert bool(torch.isnan(got[nan]).all()), "NaN by right"
+            assert bool((got[up] == float("inf")).all()) and bool((got[down] == -float("inf")).all()), "infinite by right"
+            fin = ~(nan | up | down)
+            err = (got - o[cq[b]:cq[b + 1], h]).abs()
+            assert bool((err <= tol[cq[b]:cq[b + 1], h])[fin].all()), "finite"
+    assert fd.fd_device_status(clear=True) == fd.FD_OK
