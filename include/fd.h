@@ -444,9 +444,10 @@ typedef struct fd_prompt_desc {
     int64_t k_stride_t, k_stride_h;
     int64_t v_stride_t, v_stride_h;
     int32_t total_q, total_k;   /* rows of q, and of k and v */
-    int32_t max_q, max_k;       /* the longest sequence's queries and keys as the host knows them;
-                                   0: total_q, total_k.  They plan the launch only: any values give
-                                   the same results up to rounding. */
+    int32_t max_q, max_k;       /* the longest sequence's queries and keys as the host knows them; 0:
+                                   not known.  They plan the key splits only (max_k; without it
+                                   total_k / batch; max_q not yet): any values give the same
+                                   results up to rounding. */
     int32_t causal;             /* 0: every query sees all keys of its sequence; 1: see fd_prompt */
     int32_t n_splits;           /* key splits per query tile; <= 0: planned */
     int32_t flags;              /* must be 0 */

@@ -19,6 +19,7 @@ namespace {
 using fdk::kHeadDim;
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kKeyTile = 128;   // keys per tile of fd_prompt
 
 size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -342,23 +343,41 @@ int64_t prompt_tiles(const fd_prompt_desc* d) {
     return d->total_q / (pair_heads_of(d) ? 128 : 256) + d->batch;
 }
 
-// Key splits per query tile: few tiles over long keys leave SMs idle, so where
-// the tiles (by the packed rows) take at most half of them, the keys are cut so
-// that the parts fill them, with four key tiles a part at least (a part's
-// state costs its writing and joining) and 32 parts at most.  One split against
-// planned: 64 queries, 9000 keys, 8 / 2 heads 116 -> 30 us; 200, 12000, 32 / 8
-// 152 -> 66; 512, 4000, 8 / 8 54 -> 35; but 100, 1100, 16 / 2 (9 key tiles) 22 ->
-// 24, so from 16 key tiles on.
+// Key splits per query tile.  Few tiles over long keys leave SMs idle, so the
+// keys are cut where that pays, by the time it takes in microseconds: an item
+// walks its key tiles at 1.5 each, and each wave of items costs 8 beside them
+// (first loads, epilogues); joining the parts takes 8, and 0.3 a split.  The
+// walk is the longest sequence's part or, if that is more, an average part
+// (total_k / batch keys) in each wave.  The query tiles are the most that the
+// sequences can have.  A part has four key tiles at least, there are 32 parts at
+// most, and cutting has to save an eighth.
+// One split against planned, measured: 64 queries over 9000 keys, 8 / 2 heads
+// 116 -> 30 us; 200 over 12000, 32 / 8, 152 -> 66; 512 over 4000, 8 / 8,
+// 54 -> 36; 4 single queries, 32 / 8, all over 9000 keys 124 -> 78, one over
+// 9000 and three over 100 124 -> 49.  Left whole: 64 sequences of 2 queries, 32 /
+// 8, one over 9000 keys and the others over 300 (175; in two 233, in nine 367);
+// 16 single queries over 2500, 8 / 8 (40; in two 54).
 int32_t prompt_splits(const fd_prompt_desc* d) {
     if (d->n_splits >= 1) return d->n_splits;
     const int64_t span = pair_heads_of(d) ? 128 : 256;
-    const int64_t units = (d->total_q + span - 1) / span * (pair_heads_of(d) ? d->n_q_heads / 2 : d->n_q_heads);
-    const int64_t key_tiles = ((d->max_k > 0 ? d->max_k : d->total_k) + 127) / 128;
-    if (units < 1 || key_tiles < 16) return 1;
-    const int64_t sms = fd_num_sms(-1);
-    if (units * 2 > sms) return 1;
-    const int64_t s = std::min(std::min(sms / units, key_tiles / 4), static_cast<int64_t>(32));
-    return static_cast<int32_t>(s);
+    const int64_t seqs = std::min(d->batch, d->total_q);   // (with queries, at most)
+    if (seqs < 1) return 1;
+    const double units = static_cast<double>((d->total_q + seqs * (span - 1)) / span) *
+                         (pair_heads_of(d) ? d->n_q_heads / 2 : d->n_q_heads);
+    const double all_tiles = static_cast<double>(d->total_k) / kKeyTile / d->batch;   // of a sequence on average
+    const int64_t key_tiles = ((d->max_k > 0 ? d->max_k : (d->total_k + d->batch - 1) / d->batch) + kKeyTile - 1) / kKeyTile;
+    if (key_tiles < 16) return 1;
+    const int sms = fd_num_sms(-1);
+    if (sms < 1) return 1;
+    auto time = [&](int64_t s) {
+        const double waves = std::ceil(units * s / sms);
+        const double walk = std::max(static_cast<double>((key_tiles + s - 1) / s), waves * all_tiles / s);
+        return 1.5 * walk + 8.0 * waves + (s > 1 ? 8.0 + 0.3 * s : 0.0);
+    };
+    int64_t best = 1;
+    for (int64_t s = 2; s <= std::min(key_tiles / 4, static_cast<int64_t>(32)); ++s)
+        if (time(s) < time(best)) best = s;
+    return time(best) < 0.875 * time(1) ? static_cast<int32_t>(best) : 1;
 }
 
 // 3-D map over packed rows: dims (head_dim, rows, heads), boxes of 64 dims x

@@ -126,3 +126,43 @@ def test_prompt_many_special_values(where, value, n_splits):
             err = (got - o[cq[b]:cq[b + 1], h]).abs()
             assert bool((err <= tol[cq[b]:cq[b + 1], h])[fin].all()), "finite"
     assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+# ------------------------------------------------------------------ the key splits' plan
+def planned(lens, keys, hq, hkv, known=True):
+    """Split count that fd_prompt plans: its workspace's size over one split's."""
+    q = torch.empty(sum(lens), hq, D, dtype=torch.float16, device=DEV)
+    k = torch.empty(sum(keys), hkv, D, dtype=torch.float16, device=DEV)
+    kw = dict(batch=len(lens), max_q=max(lens) if known else 0, max_k=max(keys) if known else 0)
+    size = fd.fd_prompt_workspace_size(fd.make_prompt_desc(q, k, k, **kw))
+    return size // (q.shape[0] * hq * 130 * 4) if size else 1
+
+
+def test_prompt_plan_counts_every_sequence():
+    """Each sequence has a query tile of its own: many short ones fill the SMs, and
+    cutting their keys only adds parts."""
+    assert planned([2] * 64, [9000] + [300] * 63, 32, 8) == 1
+    assert planned([1] * 100, [12000] + [200] * 99, 8, 8) == 1
+    assert planned([1] * 64, [9000] * 64, 16, 2) == 1
+    # without max_k the keys of all sequences together are no sequence's
+    assert planned([1] * 64, [300] * 64, 8, 2, known=False) == 1
+    assert planned([1] * 16, [2500] * 16, 8, 8, known=False) == 1
+    # one request, or a few, with long keys
+    assert planned([64], [9000], 8, 2) > 8 and planned([64], [9000], 8, 2, known=False) > 8
+    assert planned([1] * 4, [9000, 100, 100, 100], 32, 8) > 1
+    assert planned([1] * 4, [9000] * 4, 32, 8) == 2
+
+
+@pytest.mark.parametrize("known", [True, False])
+def test_prompt_ragged_short_queries(known):
+    """What the plan leaves whole and what it cuts, against the definition."""
+    for lens, keys, hq, hkv in (([2] * 20, [3000] + [100] * 19, 8, 2), ([1, 3, 0, 2], [4000, 50, 10, 700], 6, 2)):
+        q, k, v, cq, ck = prompt_case(41, "bf16", lens, keys, hq, hkv)
+        d = fd.make_prompt_desc(q, k, v, batch=len(lens), max_k=max(keys) if known else 0)
+        size = fd.fd_prompt_workspace_size(d)
+        out, lse = torch.full(q.shape, NAN, device=DEV), torch.full(q.shape[:2], NAN, device=DEV)
+        ws = torch.full((size,), 0xA5, dtype=torch.uint8, device=DEV) if size else None
+        fd.check(fd.fd_prompt(d, q, k, v, i32(cq), i32(ck), out, lse, ws))
+        o, z, tol, ltol = ref.prompt(q, k, v, cq, ck, True, torch.float32)
+        ref.close(out, o, tol, "out")
+        ref.close(lse, z, ltol, "lse")
