@@ -81,6 +81,7 @@ class FdKvScales(ctypes.Structure):
         ("v_stride_b", ctypes.c_int64), ("v_stride_h", ctypes.c_int64), ("v_stride_n", ctypes.c_int64),
         ("block", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
+    shape = None    # (leading, KV heads, blocks) of the tensors, by make_scales
 
 
 class FdStoreDesc(ctypes.Structure):
@@ -216,6 +217,17 @@ def _nbytes(x) -> int:
     return 0 if x is None else x.numel() * x.element_size()
 
 
+def _check_scales(desc, scales: FdKvScales) -> None:
+    """make_scales' tensors cover the cache of a decode or store descriptor (the C ABI sees no extents)."""
+    if scales.shape is None:
+        return
+    lead, heads, blocks = scales.shape
+    page = desc.page_size
+    tokens = page if page > 0 else desc.kv_extent
+    if lead < (desc.kv_extent if page > 0 else desc.batch) or heads < desc.n_kv_heads or blocks * scales.block < tokens:
+        raise ValueError(f"scales {scales.shape} of {scales.block}-token blocks do not cover the cache")
+
+
 def check(status: int, what: str = "") -> int:
     if int(status) < 0:
         raise FdError(status, what)
@@ -314,6 +326,7 @@ def fd_decode_static(desc: FdDesc, q, k_cache, v_cache, seqlens, block_table, ou
 def fd_decode_scaled(desc: FdDesc, scales: FdKvScales, q, k_cache, v_cache, seqlens, block_table, out, lse,
                      workspace, workspace_bytes: int | None = None, stream=None) -> int:
     """fd_decode over an E4M3 cache with a scale per (block of tokens, KV head); see make_scales."""
+    _check_scales(desc, scales)
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     return int(_load().fd_decode_scaled(ctypes.byref(desc), ctypes.byref(scales), _ptr(q), _ptr(k_cache),
                                         _ptr(v_cache), _ptr(seqlens), _ptr(block_table), _ptr(out), _ptr(lse),
@@ -323,6 +336,10 @@ def fd_decode_scaled(desc: FdDesc, scales: FdKvScales, q, k_cache, v_cache, seql
 def fd_cache_store(desc: FdStoreDesc, scales: FdKvScales, k, v, slots, k_cache, v_cache, stream=None) -> int:
     """New K/V rows into an E4M3 cache at `slots` (int64), quantised with a power-of-two
     scale per (block of tokens, KV head); writes the cache and the scales."""
+    _check_scales(desc, scales)
+    if slots is not None and not isinstance(slots, int):
+        if slots.element_size() != 8 or slots.numel() < desc.n_tokens or not slots.is_contiguous():
+            raise ValueError(f"slots must be {desc.n_tokens} contiguous int64")
     return int(_load().fd_cache_store(ctypes.byref(desc), ctypes.byref(scales), _ptr(k), _ptr(v), _ptr(slots),
                                       _ptr(k_cache), _ptr(v_cache), _stream(stream)))
 
@@ -417,11 +434,14 @@ def make_scales(k_scales, v_scales, *, block: int) -> FdKvScales:
     for t in (k_scales, v_scales):
         if t.dim() != 3 or t.dtype != torch.float32:
             raise ValueError("scales must be float32 tensors of 3 dimensions")
+    if k_scales.shape != v_scales.shape:
+        raise ValueError("k_scales and v_scales must have the same shape")
     s.k, s.v = k_scales.data_ptr(), v_scales.data_ptr()
     s.k_stride_b, s.k_stride_h, s.k_stride_n = k_scales.stride()
     s.v_stride_b, s.v_stride_h, s.v_stride_n = v_scales.stride()
     s.block = int(block)
     s.reserved = 0
+    s.shape = tuple(k_scales.shape)
     s._keep = (k_scales, v_scales)
     return s
 
@@ -454,9 +474,15 @@ def make_store_desc(k, v, k_cache, v_cache, *, page_size: int = 0) -> FdStoreDes
 
 
 def make_page_desc(block_table, free_pages, slots, *, page_size: int, n_pages: int) -> FdPageDesc:
-    """Descriptor for a table [B, max_pages_per_seq] (contiguous int32), the free stack and the slot map."""
+    """Descriptor for a table [B, max_pages_per_seq] (contiguous int32), the free stack (int32)
+    and the slot map (int64)."""
+    import torch
     if block_table.dim() != 2 or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous [B, max_pages_per_seq] tensor")
+    if block_table.dtype != torch.int32 or free_pages.dtype != torch.int32 or not free_pages.is_contiguous():
+        raise ValueError("block_table and free_pages must be contiguous int32 tensors")
+    if slots.dtype != torch.int64 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 tensor")
     d = FdPageDesc()
     d.batch, d.max_pages_per_seq = block_table.shape
     d.page_size, d.n_pages = int(page_size), int(n_pages)

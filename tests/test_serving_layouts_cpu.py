@@ -101,3 +101,43 @@ def test_store_refuses_scales_that_several_blocks_share(fd, field, paged):  # no
         d.page_size, d.kv_extent, d.batch = 0, 64, 5
     setattr(s, field, 0)
     assert fd.fd_cache_store(d, s, 1024, 1024, 1024, 1024, 1024, stream=0) == fd.FD_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ the binding's own checks
+def test_page_desc_refuses_other_types(fd):  # noqa: F811
+    """The kernel writes 8 bytes a slot and reads 4 a page: tensors of other types are shorter or longer than they look."""
+    i32, i64 = (lambda *n: torch.zeros(*n, dtype=torch.int32)), (lambda *n: torch.zeros(*n, dtype=torch.int64))
+    d = fd.make_page_desc(i32(2, 8), i32(4), i64(10), page_size=16, n_pages=20)
+    assert (d.batch, d.max_pages_per_seq, d.n_free_max, d.n_slots) == (2, 8, 4, 10)
+    for table, free, slots in ((i32(2, 8), i32(4), i32(10)), (i64(2, 8), i32(4), i64(10)), (i32(2, 8), i64(4), i64(10)),
+                               (i32(2, 8), i32(4), i64(20)[::2]), (i32(2, 8), i32(8)[::2], i64(10)), (i32(16), i32(4), i64(10))):
+        with pytest.raises(ValueError):
+            fd.make_page_desc(table, free, slots, page_size=16, n_pages=20)
+
+
+@pytest.mark.parametrize("page", [64, 0])
+def test_scales_and_slots_have_to_cover_the_call(fd, page):  # noqa: F811
+    """The C ABI sees addresses only; the binding has the tensors and compares them."""
+    kc, vc = (torch.zeros(3, 2, 64, 128).to(torch.float8_e4m3fn) for _ in range(2))
+    rows = torch.zeros(5, 2, 128, dtype=torch.float16)
+    store = fd.make_store_desc(rows, rows, kc, vc, page_size=page)
+    q = torch.zeros(3, 8, 128, dtype=torch.float16)
+    decode = fd.make_desc(q, kc, vc, page_size=page, max_pages_per_seq=2, max_seqlen=64, n_splits=1)
+    store_0, decode_0 = fd.FdStoreDesc.from_buffer_copy(store), decode.copy()
+    store_0.n_tokens, decode_0.batch = 0, 0                    # (nothing is enqueued: the checks alone)
+    scales = lambda *n: fd.make_scales(torch.ones(*n), torch.ones(*n), block=16)
+    slots = torch.zeros(5, dtype=torch.int64)
+    call_store = lambda d, s, at: fd.fd_cache_store(d, s, rows, rows, at, kc, vc, stream=0)
+    call_decode = lambda d, s: fd.fd_decode_scaled(d, s, q, kc, vc, 1024, 1024, 1024, None, None, 0, stream=0)
+    assert call_store(store_0, scales(3, 2, 4), slots) == fd.FD_OK
+    assert call_decode(decode_0, scales(3, 2, 4)) == fd.FD_OK
+    for n in ((2, 2, 4), (3, 1, 4), (3, 2, 3)):
+        with pytest.raises(ValueError):
+            call_store(store, scales(*n), slots)
+        with pytest.raises(ValueError):
+            call_decode(decode, scales(*n))
+    for at in (torch.zeros(5, dtype=torch.int32), torch.zeros(4, dtype=torch.int64), torch.zeros(10, dtype=torch.int64)[::2]):
+        with pytest.raises(ValueError):
+            call_store(store, scales(3, 2, 4), at)
+    with pytest.raises(ValueError):
+        fd.make_scales(torch.ones(3, 2, 4), torch.ones(3, 2, 5), block=16)
