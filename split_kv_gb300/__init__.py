@@ -217,6 +217,16 @@ def _nbytes(x) -> int:
     return 0 if x is None else x.numel() * x.element_size()
 
 
+def _check_out(out, lse, out_dtype: int, rows: int, head_dim: int) -> None:
+    """The tensors that a call writes are as large as its descriptor says."""
+    if out is not None and not isinstance(out, int):
+        if out.element_size() != (4 if out_dtype == FD_F32 else 2) or out.numel() < rows * head_dim or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous, of the descriptor's out_dtype, with {rows} rows")
+    if lse is not None and not isinstance(lse, int):
+        if lse.element_size() != 4 or lse.numel() < rows or not lse.is_contiguous():
+            raise ValueError(f"lse must be {rows} contiguous float32")
+
+
 def _check_scales(desc, scales: FdKvScales) -> None:
     """make_scales' tensors cover the cache of a decode or store descriptor (the C ABI sees no extents)."""
     if scales.shape is None:
@@ -327,6 +337,7 @@ def fd_decode_scaled(desc: FdDesc, scales: FdKvScales, q, k_cache, v_cache, seql
                      workspace, workspace_bytes: int | None = None, stream=None) -> int:
     """fd_decode over an E4M3 cache with a scale per (block of tokens, KV head); see make_scales."""
     _check_scales(desc, scales)
+    _check_out(out, lse, desc.out_dtype, desc.batch * max(desc.q_len, 1) * desc.n_q_heads, desc.head_dim)
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     return int(_load().fd_decode_scaled(ctypes.byref(desc), ctypes.byref(scales), _ptr(q), _ptr(k_cache),
                                         _ptr(v_cache), _ptr(seqlens), _ptr(block_table), _ptr(out), _ptr(lse),
@@ -360,6 +371,7 @@ def fd_prompt_workspace_size(desc: FdPromptDesc) -> int:
 def fd_prompt(desc: FdPromptDesc, q, k, v, cu_q, cu_k, out, lse, workspace=None,
               workspace_bytes: int | None = None, stream=None) -> int:
     """Attention over whole prompts: packed sequences, causal or full."""
+    _check_out(out, lse, desc.out_dtype, desc.total_q * desc.n_q_heads, desc.head_dim)
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     return int(_load().fd_prompt(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(out),
                                  _ptr(lse), _ptr(workspace), int(wb), _stream(stream)))

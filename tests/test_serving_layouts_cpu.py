@@ -141,3 +141,22 @@ def test_scales_and_slots_have_to_cover_the_call(fd, page):  # noqa: F811
             call_store(store, scales(3, 2, 4), at)
     with pytest.raises(ValueError):
         fd.make_scales(torch.ones(3, 2, 4), torch.ones(3, 2, 5), block=16)
+
+
+def test_outputs_have_to_be_as_large_as_the_descriptor_says(fd):  # noqa: F811
+    """A 16-bit out under a descriptor for 32 bits (its default) would be written twice over."""
+    q, k = torch.zeros(5, 8, 128, dtype=torch.bfloat16), torch.zeros(5, 2, 128, dtype=torch.bfloat16)
+    d = fd.make_prompt_desc(q, k, k, batch=0)
+    call = lambda out, lse: fd.fd_prompt(d, q, k, k, None, None, out, lse, None, stream=0)
+    f32, lse = torch.zeros(5, 8, 128), torch.zeros(5, 8)
+    assert call(f32, lse) == call(f32, None) == call(1024, 1024) == fd.FD_OK      # (batch 0: nothing is enqueued)
+    for out, z in ((f32.bfloat16(), lse), (f32[:4], lse), (f32.transpose(0, 1), lse), (f32, lse[:4]), (f32, lse.half()),
+                   (f32, lse.double()), (f32, lse.t())):
+        with pytest.raises(ValueError):
+            call(out, z)
+    kc = torch.zeros(3, 2, 64, 128).to(torch.float8_e4m3fn)
+    s = fd.make_scales(torch.ones(3, 2, 4), torch.ones(3, 2, 4), block=16)
+    d = fd.make_desc(q[:3], kc, kc, max_seqlen=64, n_splits=1)
+    for out, z in ((f32.bfloat16(), lse), (f32[:2], lse), (f32, lse[:2])):
+        with pytest.raises(ValueError):
+            fd.fd_decode_scaled(d, s, q, kc, kc, 1024, None, out, z, None, 0, stream=0)
