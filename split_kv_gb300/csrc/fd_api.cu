@@ -38,6 +38,13 @@ WsLayout ws_layout(int64_t rows, int64_t splits) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// Addresses of out and lse: multiples of their elements' size.
+bool outputs_aligned(int32_t out_dtype, const void* out, const float* lse) {
+    return aligned_to(out, out_dtype == FD_F32 ? 4 : 2) && aligned_to(lse, 4);
+}
+
 // A stride in elements of `esize` bytes is usable by TMA: a multiple of 16 bytes.
 bool stride_ok(int64_t s, int esize = 2) {
     return s >= 0 && (s * esize) % 16 == 0 && s < (int64_t(1) << 38);
@@ -530,7 +537,9 @@ fd_status fd_decode_scaled(const fd_desc* desc, const fd_kv_scales* scales, cons
     st = check_scales(scales, desc->page_size);
     if (st != FD_OK) return st;
     if (desc->batch == 0) return FD_OK;   // (an empty tensor's address is null)
-    if (out == nullptr) return FD_ERR_INVALID_ARG;
+    if (out == nullptr || !outputs_aligned(desc->out_dtype, out, lse) || !aligned_to(seqlens, 4) ||
+        !aligned_to(block_table, 4))
+        return FD_ERR_INVALID_ARG;
     const int32_t S = splits_for(desc);
     if (S < 1) return static_cast<fd_status>(S < 0 ? S : FD_ERR_INVALID_ARG);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -682,8 +691,7 @@ fd_status fd_prompt(const fd_prompt_desc* d, const void* q, const void* k, const
         (d->total_k > 0 && (k == nullptr || v == nullptr)))
         return FD_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return FD_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(cu_q) & 3u) != 0 || (reinterpret_cast<uintptr_t>(cu_k) & 3u) != 0)
-        return FD_ERR_INVALID_ARG;
+    if (!aligned_to(cu_q, 4) || !aligned_to(cu_k, 4) || !outputs_aligned(d->out_dtype, out, lse)) return FD_ERR_INVALID_ARG;
     const int32_t S = prompt_splits(d);
     if (S < 1) return static_cast<fd_status>(S < 0 ? S : FD_ERR_INVALID_ARG);
     const WsLayout w = ws_layout(static_cast<int64_t>(d->total_q) * d->n_q_heads, S);

@@ -160,3 +160,17 @@ def test_outputs_have_to_be_as_large_as_the_descriptor_says(fd):  # noqa: F811
     for out, z in ((f32.bfloat16(), lse), (f32[:2], lse), (f32, lse[:2])):
         with pytest.raises(ValueError):
             fd.fd_decode_scaled(d, s, q, kc, kc, 1024, None, out, z, None, 0, stream=0)
+
+
+@pytest.mark.parametrize("out_dtype,out,lse,aux", [("f32", 1026, 1024, 1024), ("f16", 1025, 1024, 1024), ("bf16", 1024, 1026, 1024),
+                                                   ("f32", 1024, 1024, 1026)])
+def test_addresses_are_multiples_of_their_elements(fd, out_dtype, out, lse, aux):  # noqa: F811
+    code = {"f32": fd.FD_F32, "f16": fd.FD_F16, "bf16": fd.FD_BF16}[out_dtype]
+    d = _prompt(fd)
+    d.out_dtype = code
+    assert fd.fd_prompt(d, 1024, 1024, 1024, aux, 1024, out, lse, None, 0, stream=0) == fd.FD_ERR_INVALID_ARG
+    d = _decode(fd, kv_dtype=fd.FD_E4M3, page_size=64, max_pages_per_seq=4, out_dtype=code)
+    assert fd.fd_decode_scaled(d, _scales(fd), 1024, 1024, 1024, aux, 1024, out, lse, 1024, 1 << 30,
+                               stream=0) == fd.FD_ERR_INVALID_ARG
+    assert fd.fd_decode_scaled(d, _scales(fd), 1024, 1024, 1024, 1024, 1026, 1024, 1024, 1024, 1 << 30,
+                               stream=0) == fd.FD_ERR_INVALID_ARG
