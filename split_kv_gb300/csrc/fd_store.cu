@@ -240,6 +240,8 @@ __device__ __forceinline__ void store_item(const T* src, int64_t src_t, uint8_t*
 // then the short ones (a step's) are taken by a warp each, in turn.  The slots
 // of the tile and of the rows that its last unit may go on with are read once
 // into shared memory, so that the chain is slots -> rows and old scale -> stores.
+// (Heads per CTA 1 / 2 / 4 / 8: 10194 prompt rows of 8 heads 26.2 / 20.2 / 23.9 / 32.2 us,
+// 256 single rows 6.7 / 5.0 / 5.7 / 9.1, 64 2.9 / 3.4 / 4.2 / 6.5.)
 constexpr int kHeads = 2;
 constexpr int kAhead = 256;             // slots in shared memory
 constexpr int kLong = 2 * kKeep;        // rows that one warp keeps
@@ -360,9 +362,16 @@ cudaError_t launch_store_tile(const StoreParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_store_t(const StoreParams& p, cudaStream_t stream) {
-    // few rows, each likely a unit of its own (a decode step): small tiles keep
-    // a warp to one item; many: tiles of 64 leave few CTAs without a unit
-    return p.n_tokens <= 256 ? launch_store_tile<T, 4>(p, stream) : launch_store_tile<T, 64>(p, stream);
+    // Rows of the list per CTA.  Single rows of many requests (a decode step) are
+    // a unit each, so that small tiles keep a warp to few items; a prompt's rows
+    // are few units, of which large tiles leave hardly a CTA without one.  From
+    // rows alone the two cannot be told apart, and the first lose more.  8 heads,
+    // tiles of 4 / 8 / 64: 256 single rows 5.0 / 5.7 / 23.3 us, of one prompt 3.3 /
+    // 3.0 / 3.1 (blocks of 16); 400: 6.3 / 5.8 / 23.6, 3.7 / 3.0 / 3.2; 1024: 13.3 /
+    // 12.4 / 35.5, 6.2 / 4.8 / 4.2; 4000 of one prompt 18.5 / 12.9 / 6.5.
+    if (p.n_tokens <= 256) return launch_store_tile<T, 4>(p, stream);
+    if (p.n_tokens <= 1024) return launch_store_tile<T, 8>(p, stream);
+    return launch_store_tile<T, 64>(p, stream);
 }
 
 }  // namespace

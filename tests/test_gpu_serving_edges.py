@@ -12,7 +12,7 @@ import torch
 import serving_ref as ref
 import split_kv_gb300 as fd
 from test_gpu_serving import (DEV, NAN, D, _clean_status, _lib, cumulative, gen, i32, prompt_case, randn,  # noqa: F401
-                              run_prompt, run_tables, table_case)
+                              run_prompt, run_store, run_tables, store_case, table_case)
 
 pytestmark = pytest.mark.gpu
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -166,3 +166,18 @@ def test_prompt_ragged_short_queries(known):
         o, z, tol, ltol = ref.prompt(q, k, v, cq, ck, True, torch.float32)
         ref.close(out, o, tol, "out")
         ref.close(lse, z, ltol, "lse")
+
+
+# ------------------------------------------------------------------ the store's tiles
+@pytest.mark.parametrize("n", [257, 1024, 1025])
+def test_store_single_rows_of_many_requests(n):
+    """A step of as many requests as decide the tile of the launch, some skipped."""
+    held = [(k * 977) % 300 for k in range(n)]
+    k, v, slots, caches, scales = store_case(n, "bf16", [1] * n, held, 2, 16, 16)
+    slots[5::11] = -1
+    run_store(k, v, slots, caches, scales, 16, 16)
+
+
+@pytest.mark.parametrize("lens,held", [([300, 1, 90], [7, 63, 0]), ([1000], [5]), ([3] * 120, [k % 70 for k in range(120)])])
+def test_store_prompt_rows_across_tiles(lens, held):
+    run_store(*store_case(len(lens), "f16", lens, held, 3, 64, 32), 64, 32)
