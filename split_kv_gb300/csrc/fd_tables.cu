@@ -161,11 +161,16 @@ __global__ void __launch_bounds__(1024) fd_page_tables_kernel(const PageParams p
 }  // namespace
 
 cudaError_t launch_page_tables(const PageParams& p, cudaStream_t stream) {
-    // tokens per CTA of the cluster: a step's few tokens stay in one CTA
-    constexpr int64_t kTokensPerCta = 2048;
+    // Time is latency: more threads mean longer barriers and scans, fewer mean
+    // more rounds in turn; more CTAs share the rounds, up to the portable 8.
+    // Threads 256 / 512 / 1024: 64 requests of one token 3.2 / 3.8 / 6.2 us, 300
+    // 5.3 / 4.2 / 6.6, 8000 35.0 / 28.8 / 34.9; 8000 tokens of 8 requests 4.3 / 4.0 /
+    // 6.1, 32000 10.1 / 7.2 / 8.1, 60000 17.0 / 10.8 / 10.5.  Tokens per CTA 512 / 1024 /
+    // 2048 (512 threads): 2000 tokens of 8 requests 3.5 / 4.1 / 5.0, 8000 4.0 / 4.0 / 5.1.
+    constexpr int64_t kTokensPerCta = 512;
     const int64_t want = (p.n_slots + kTokensPerCta - 1) / kTokensPerCta;
     const int ctas = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
-    const int threads = p.n_slots <= 256 && p.batch <= 256 ? 256 : 1024;
+    const int threads = p.n_slots <= 256 && p.batch <= 256 ? 256 : p.n_slots <= 49152 ? 512 : 1024;
     const size_t smem = (3 * static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
     // the limit of the largest batch, whatever this call's is (the default of
     // 48 KB counts the static arrays too): calls of two threads never lower it
