@@ -154,6 +154,11 @@ def test_outputs_have_to_be_as_large_as_the_descriptor_says(fd):  # noqa: F811
                    (f32, lse.double()), (f32, lse.t())):
         with pytest.raises(ValueError):
             call(out, z)
+    # the other way round: 32 bits under a descriptor for 16
+    d = fd.make_prompt_desc(q, k, k, batch=0, out_dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        call(f32, lse)
+    assert call(f32.bfloat16(), lse) == fd.FD_OK
     kc = torch.zeros(3, 2, 64, 128).to(torch.float8_e4m3fn)
     s = fd.make_scales(torch.ones(3, 2, 4), torch.ones(3, 2, 4), block=16)
     d = fd.make_desc(q[:3], kc, kc, max_seqlen=64, n_splits=1)
@@ -174,3 +179,10 @@ def test_addresses_are_multiples_of_their_elements(fd, out_dtype, out, lse, aux)
                                stream=0) == fd.FD_ERR_INVALID_ARG
     assert fd.fd_decode_scaled(d, _scales(fd), 1024, 1024, 1024, 1024, 1026, 1024, 1024, 1024, 1 << 30,
                                stream=0) == fd.FD_ERR_INVALID_ARG
+
+
+def test_addresses_are_taken_of_tensors_integers_and_none(fd):  # noqa: F811
+    t = torch.zeros(3)
+    assert fd._ptr(t) == t.data_ptr() and fd._ptr(1024) == 1024 and fd._ptr(None) is None
+    with pytest.raises(TypeError):
+        fd._ptr("1024")
