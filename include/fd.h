@@ -380,8 +380,9 @@ typedef struct fd_store_desc {
  *    the one they need.  If it grew, the rows before them in the block are
  *    rewritten for it (exact but for values that become E4M3 subnormals).
  * Each value is rounded once to the nearest E4M3 number of its block (ties to
- * even); an infinity or NaN is stored as NaN.  Rows of the block behind the
- * new ones are left as they are. */
+ * even; under a larger scale that was there and is no power of two the quotient
+ * is rounded to 32 bits first); an infinity or NaN is stored as NaN.  Rows of
+ * the block behind the new ones are left as they are. */
 fd_status fd_cache_store(const fd_store_desc* desc, const fd_kv_scales* scales, const void* k,
                          const void* v, const int64_t* slots, void* k_cache, void* v_cache,
                          void* stream);
@@ -463,6 +464,12 @@ size_t fd_prompt_workspace_size(const fd_prompt_desc* desc);
  * causal: the queries are the last nq of the nk positions, query i sees keys
  * j <= i + nk - nq (a prompt's chunk behind keys that are there already has nk >
  * nq).  A query that sees no key gets out = 0 and lse = -inf.
+ * Arithmetic: scores, exponentials and sums are held in 32 bits; for the product
+ * with V each weight exp(s_ij - reference) is rounded to the type of q (half a
+ * step: 2^-8 of it for FD_BF16; 2^-11 for FD_F16, and 2^-25 where that is more),
+ * so that out is off by up to that part of sum_j softmax(s_i)_j |v_j| whatever
+ * out_dtype is.  lse has the weights unrounded.  (fd_decode carries the weights'
+ * low parts too.)
  * A key's or value's infinities and NaN reach only the queries that see it
  * (rows that share a tile of 128 with such a value of V behind their last key
  * are computed a second time, slowly).
