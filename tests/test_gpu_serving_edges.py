@@ -11,8 +11,9 @@ import torch
 
 import serving_ref as ref
 import split_kv_gb300 as fd
-from test_gpu_serving import (DEV, NAN, D, _clean_status, _lib, cumulative, gen, i32, prompt_case, randn,  # noqa: F401
-                              run_prompt, run_store, run_tables, store_case, table_case)
+from test_gpu_serving import (DEV, NAN, D, _clean_status, _lib, check_scaled, gen, i32,  # noqa: F401
+                              prompt_case, randn, run_prompt, run_scaled, run_store, run_tables,
+                              scaled_case, store_case, table_case)
 
 pytestmark = pytest.mark.gpu
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -181,3 +182,138 @@ def test_store_single_rows_of_many_requests(n):
 @pytest.mark.parametrize("lens,held", [([300, 1, 90], [7, 63, 0]), ([1000], [5]), ([3] * 120, [k % 70 for k in range(120)])])
 def test_store_prompt_rows_across_tiles(lens, held):
     run_store(*store_case(len(lens), "f16", lens, held, 3, 64, 32), 64, 32)
+
+
+# ------------------------------------------------------------------ calls that the contracts allow
+def test_prompt_special_values_of_many_sequences():
+    """More sequences than are sorted: the rows to redo are found in the order of the sequences."""
+    lens = [int(x) for x in np.random.default_rng(5).integers(1, 60, size=140)]
+    q, k, v, cq, ck = prompt_case(51, "f16", lens, lens, 4, 2)
+    for b in range(0, 140, 3):                     # behind the first query of every third sequence
+        v[cq[b + 1] - 1, b % 2, b % D] = NAN
+    out, _ = run_prompt(q, k, v, cq, ck, True)
+    o, _, tol, _ = ref.prompt(q, k, torch.nan_to_num(v), cq, ck, True, torch.float32)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    for b in range(0, 140, 3):
+        hit[cq[b + 1] - 1, 2 * (b % 2):2 * (b % 2) + 2, b % D] = True
+    assert bool(torch.isnan(out[hit]).all())
+    assert bool(((out.double() - o).abs() <= tol)[~hit].all())
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 1)])
+def test_prompt_head_stride_of_one_head_is_never_used(hq, hkv):
+    q, k, v, cq, ck = prompt_case(52, "bf16", [150], [150], hq, hkv)
+    zero = lambda x: x.as_strided(x.shape, (x.stride(0), 0, 1))
+    want = run_prompt(q, k, v, cq, ck, True)
+    got = run_prompt(zero(q) if hq == 1 else q, zero(k), zero(v), cq, ck, True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("q_len,G", [(16, 16), (16, 2), (1, 128), (5, 13)])
+def test_scaled_decode_wide_query_blocks(q_len, G):
+    lens = [3, 500, 0, 1025]
+    case = scaled_case(G, "bf16", lens, q_len, G, 1, 32, 16)
+    check_scaled(*case, lens, 32, 16)
+
+
+def test_scaled_decode_reads_scales_that_heads_and_blocks_share():
+    """One K scale for all heads, one V scale for all blocks of a head: strides of 0 are the decode's to read."""
+    lens = [700, 33]
+    q, caches, scales, table = scaled_case(53, "f16", lens, 1, 8, 2, 16, 16)
+    shared = [scales[0][:, :1].expand(-1, 2, -1), scales[1][:1].expand(scales[1].shape[0], -1, -1)]
+    check_scaled(q, caches, shared, table, lens, 16, 16)
+
+
+def test_prompt_captured_with_key_splits_replays_on_new_inputs():
+    q, k, v, cq, ck = prompt_case(54, "bf16", [60, 5], [4000, 300], 6, 2)
+    d = fd.make_prompt_desc(q, k, v, batch=2, max_k=4000)
+    ws = torch.empty(fd.fd_prompt_workspace_size(d), dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 0
+    out, lse, a, b = torch.zeros(q.shape, device=DEV), torch.zeros(q.shape[:2], device=DEV), i32(cq), i32(ck)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run = lambda: fd.check(fd.fd_prompt(d, q, k, v, a, b, out, lse, ws))
+        run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            run()
+        for cut in (4000, 100, 4300):              # the sequences' border moves on the GPU
+            for x in (q, k, v):
+                x.copy_(torch.randn(x.shape, generator=gen(cut), device=DEV))
+            b.copy_(i32([0, cut, 4300]))
+            graph.replay()
+            side.synchronize()
+            o, z, tol, ltol = ref.prompt(q, k, v, cq, [0, cut, 4300], True, torch.float32)
+            ref.close(out, o, tol, "out")
+            ref.close(lse, z, ltol, "lse")
+
+
+def test_calls_on_two_streams_at_once():
+    """Prompts, stores and decodes of two requests' programs, each on a stream and with buffers of its own."""
+    jobs = []
+    for s in range(2):
+        q, k, v, cq, ck = prompt_case(60 + s, "bf16", [700 + 90 * s, 33], [900, 33 + s], 8, 2)
+        lens = [4000 + s, 77]
+        jobs.append((torch.cuda.Stream(), (q, k, v, cq, ck), (*scaled_case(70 + s, "f16", lens, 1, 8, 2, 16, 16), lens)))
+    want = [(run_prompt(*p, True), run_scaled(*c[:4], c[4], 16, 16)) for _, p, c in jobs]
+    got = [[], []]
+
+    def work(i):
+        stream, p, c = jobs[i]
+        torch.cuda.set_device(DEV)
+        with torch.cuda.stream(stream):
+            for _ in range(10):
+                got[i].append((run_prompt(*p, True), run_scaled(*c[:4], c[4], 16, 16)))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 10
+        for (po, pl), (so, sl) in got[i]:
+            assert torch.equal(po.nan_to_num(7), want[i][0][0].nan_to_num(7)) and torch.equal(pl.nan_to_num(7), want[i][0][1].nan_to_num(7))
+            assert torch.equal(so, want[i][1][0]) and torch.equal(sl, want[i][1][1])
+
+
+def test_cache_offsets_past_32_bits():
+    """A pool of 70000 pages, 4.6 GB each of K and V: rows stored and read at its end, as in a small pool."""
+    H, page, block, far = 8, 64, 16, 70000
+    pages = [far - 1, 3, far - 7, 35001]
+    n = 3 * page + 9
+    g = gen(80)
+    k, v = randn(g, "bf16", n, H, D), randn(g, "bf16", n, H, D)
+    q = randn(g, "bf16", 1, 1, 16, D)
+    got = []
+    for pool, where in ((far, pages), (4, [3, 0, 1, 2])):
+        caches = [torch.zeros(pool, H, page, D, dtype=torch.uint8, device=DEV).view(ref.F8) for _ in range(2)]
+        scales = [torch.ones(pool, H, page // block, device=DEV) for _ in range(2)]
+        at = torch.tensor(where, device=DEV)
+        t = torch.arange(n, device=DEV)
+        slots = at[t // page] * page + t % page
+        fd.check(fd.fd_cache_store(fd.make_store_desc(k, v, *caches, page_size=page), fd.make_scales(*scales, block=block),
+                                   k, v, slots, *caches))
+        out, lse = run_scaled(q, caches, scales, at[None].to(torch.int32), [n], page, block)
+        got.append([out, lse] + [x.view(torch.uint8)[at] for x in caches] + [s[at] for s in scales])
+        del caches, scales
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert float(got[0][0].abs().max()) > 0
+
+
+def test_prompt_offsets_past_32_bits():
+    """Rows 131072 elements apart: the last ones lie 9 GB behind the first."""
+    n, last = 35000, 200
+    g = gen(81)
+    wide = torch.zeros(n, 1024, D, dtype=torch.bfloat16, device=DEV)
+    q, k, v = wide[:, :4], wide[:, 500:502], wide[:, 1022:]
+    for x in (q, k, v):
+        x[-last:] = randn(g, "bf16", last, x.shape[1], D)
+    small = [x[-last:].contiguous() for x in (q, k, v)]
+    d = fd.make_prompt_desc(q, k, v, batch=1, max_q=last, max_k=last, n_splits=1)
+    out, lse = torch.zeros(n, 4, D, device=DEV), torch.zeros(n, 4, device=DEV)
+    fd.check(fd.fd_prompt(d, q, k, v, i32([n - last, n]), i32([n - last, n]), out, lse))
+    want, wl = run_prompt(*small, [0, last], [0, last], True, n_splits=1)
+    assert torch.equal(out[-last:], want) and torch.equal(lse[-last:], wl) and not bool(out[:-last].any())
