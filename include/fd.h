@@ -395,7 +395,7 @@ typedef struct fd_page_desc {
     int32_t max_pages_per_seq;  /* row length of block_table */
     int32_t n_pages;            /* pages in the pool */
     int32_t n_free_max;         /* entries of free_pages */
-    int32_t n_slots;            /* entries of slots and positions */
+    int32_t n_slots;            /* entries of slots and positions (fd_page_tables) or of the copy list (the others) */
 } fd_page_desc;
 
 /* Page tables and slot map of one step, on the GPU: sequence b holds
@@ -485,6 +485,195 @@ size_t fd_prompt_workspace_size(const fd_prompt_desc* desc);
 fd_status fd_prompt(const fd_prompt_desc* desc, const void* q, const void* k, const void* v,
                     const int32_t* cu_q, const int32_t* cu_k, void* out, float* lse,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ======================================================================
+ * Between the projections and the paged cache: norms and rotation of a step's
+ * heads on their way into a cache, and the life of pages after fd_page_tables
+ * has given them out (shared, given back, moved).  The conventions at the head
+ * of this file hold.
+ *
+ * Pages that several sequences hold: shares[p] (device int32[n_pages]) is the
+ * number of sequences that hold page p beyond the first, so 0 for a page of one
+ * sequence and for a free one, and fd_page_tables needs to know nothing of it.
+ * A page is shared only while it is full for every sequence that holds it: a
+ * fork copies a page of which it takes a part, and a trim that ends inside a
+ * shared page replaces it by a copy.  So new tokens never go into a shared page.
+ *
+ * Both, and fd_page_compact, write down what has to be copied as a list:
+ * copy_src[i] -> copy_dst[i], i < *copy_count (device int32[n_slots] and
+ * int32[1]; entries behind are left as they are), which fd_page_copy carries out
+ * in the caches of every layer, before anything is appended.  No page is in a
+ * list as a source and as a destination.
+ * ====================================================================== */
+
+#define FD_NORM_Q 1     /* fd_rope_desc.norm: queries */
+#define FD_NORM_K 2     /* keys */
+
+/* Rows of one step: q at q + t*q_stride_t + h*q_stride_h, k and v at
+ * k_src_stride_* and v_src_stride_* likewise (slices of one projection's output,
+ * for instance).  The head dimension is contiguous, base addresses are 16-byte
+ * aligned, strides multiples of 8 elements (16 of an FD_E4M3 cache). */
+typedef struct fd_rope_desc {
+    int32_t n_tokens;           /* >= 0; 0 enqueues nothing */
+    int32_t n_q_heads;          /* >= 0 */
+    int32_t n_kv_heads;         /* >= 0; one of the two at least 1 */
+    int32_t head_dim;           /* 128 */
+    int32_t dtype;              /* of q, k, v, q_out, k_out: FD_F16 or FD_BF16 */
+    int32_t cache_dtype;        /* dtype, or FD_E4M3 (unused without a cache) */
+    int32_t w_dtype;            /* of the weights: FD_F32, FD_F16 or FD_BF16 */
+    int32_t norm;               /* FD_NORM_* bits */
+    int32_t rot_dim;            /* leading elements of a row that are rotated: 0, 16, .. 128 */
+    int32_t interleaved;        /* pairs (i, i + rot_dim/2): 0; (2i, 2i+1): 1 */
+    float eps;                  /* >= 0, finite */
+    float rot_scale;            /* factor of the rotated part (1 unless a long-context scheme asks for it) */
+    float k_scale, v_scale;     /* FD_E4M3: stored = value / scale, as fd_desc's; normal numbers > 0 */
+    int64_t q_stride_t, q_stride_h;
+    int64_t k_src_stride_t, k_src_stride_h, v_src_stride_t, v_src_stride_h;
+    int64_t q_out_stride_t, q_out_stride_h, k_out_stride_t, k_out_stride_h;
+    int64_t k_stride_b, k_stride_h, k_stride_t;     /* caches, as fd_desc's */
+    int64_t v_stride_b, v_stride_h, v_stride_t;
+    int64_t q_w_stride_h, k_w_stride_h;             /* 0: the heads share their weights */
+    int64_t kv_extent;          /* contiguous: tokens per sequence; paged: pages in the pool */
+    int32_t page_size;          /* 0 = contiguous; else a power of two >= 8 */
+    int32_t batch;              /* contiguous: sequences in the cache; paged: unused */
+    int32_t flags;              /* must be 0 */
+    int32_t reserved;           /* must be 0 */
+} fd_rope_desc;
+
+/* Heads of a step's tokens: for each row x of q and k,
+ *     n = x / sqrt(sum_d x_d^2 / 128 + eps) * w         (where FD_NORM_* asks; else n = x)
+ *     y_a = rot_scale (n_a cos - n_b sin),  y_b = rot_scale (n_b cos + n_a sin)
+ * for the pairs (a, b) of its first rot_dim elements, with the angle
+ * positions[t] * inv_freq[i] of pair i; the other elements pass as n.  Rows of q
+ * go to q_out; rows of k to k_out and into the K cache at their slots, rows of v
+ * unchanged into the V cache.  fd_decode then reads the caches (FD_E4M3: with the
+ * same scales); for one with block scales, k_out and v go through fd_cache_store.
+ *  q, k, v    : device; q may be NULL with n_q_heads = 0, k with n_kv_heads = 0, v
+ *               without caches.
+ *  q_weight, k_weight : device, w_dtype, 128 per head (or for all); NULL: 1.
+ *  inv_freq   : device float[rot_dim/2], finite (NULL with rot_dim 0).
+ *  positions  : device int32[n_tokens], as fd_page_tables writes them; a row
+ *               with a negative one is left out: nothing of it is written.
+ *  slots      : device int64[n_tokens], as fd_cache_store takes them (NULL
+ *               without caches): a negative one leaves the caches as they are,
+ *               one outside them too and sets FD_ERR_DEVICE_BOUNDS; q_out and
+ *               k_out get their rows all the same.  No slot appears twice.
+ *  q_out, k_out : device, [n_tokens, heads, 128] with the strides given; each may
+ *               be its input itself with the same strides (else they do not
+ *               overlap it).  k_out may be NULL.
+ *  k_cache, v_cache : device, both or neither.
+ * Arithmetic: norms and rotation in 32 bits (sums of squares too: they overflow
+ * for values of about 1.6e18), angles as fractions of a turn in 64-bit fixed
+ * point, so that they are as exact for far positions as for near ones; each
+ * result is rounded once to its output's type.  FD_E4M3: the value times the
+ * reciprocal of the scale (rounded to 32 bits), to the nearest, ties to even,
+ * beyond 448 to 448; an infinity or NaN is stored as NaN. */
+fd_status fd_qkv_rope(const fd_rope_desc* desc, const void* q, const void* k, const void* v,
+                      const void* q_weight, const void* k_weight, const float* inv_freq,
+                      const int32_t* positions, const int64_t* slots, void* q_out, void* k_out,
+                      void* k_cache, void* v_cache, void* stream);
+
+/* Forks: sequence children[i], which holds nothing yet, gets the first keep[i]
+ * tokens of sequence parents[i].  Full pages are shared (shares goes up by one),
+ * of a page of which the fork takes a part the child gets a copy: a page of
+ * its own and an entry of the copy list.
+ *  desc          : n_slots: entries of copy_src and copy_dst, >= n_forks.
+ *  n_forks       : 0 <= n_forks <= FD_MAX_TABLE_BATCH.
+ *  parents, children, keep : device int32[n_forks]; keep NULL: all of the
+ *                  parent's tokens.  A parent may be named many times.
+ *  seqlens, seqlens_out : device int32[batch], may be the same buffer.
+ *  free_pages, free_count, free_count_out : as fd_page_tables takes them: the i-th
+ *                  copy, forks in order, is free_pages[free_count - 1 - i].
+ *  block_table   : the children's entries for their pages are written.
+ *  shares        : device int32[n_pages], in and out.
+ * All parents are read as they were before the call.  A fork out of range (an index
+ * outside the batch, a child that is its own parent, holds tokens already or is
+ * named by an earlier valid fork, keep < 0 or beyond the parent's tokens) or whose page the
+ * free list cannot cover in that order is left out: its child stays as it was.
+ * Those, a page index outside the pool, and a free count out of range set
+ * FD_ERR_DEVICE_BOUNDS in the status word. */
+fd_status fd_page_fork(const fd_page_desc* desc, int32_t n_forks, const int32_t* parents,
+                       const int32_t* children, const int32_t* keep, const int32_t* seqlens,
+                       const int32_t* free_pages, const int32_t* free_count, int32_t* block_table,
+                       int32_t* shares, int32_t* seqlens_out, int32_t* free_count_out,
+                       int32_t* copy_src, int32_t* copy_dst, int32_t* copy_count, void* stream);
+
+/* Trims: sequence b keeps its first keep[b] tokens (drafts that were not taken,
+ * a finished request with 0); keep[b] < 0 or >= seqlens[b] leaves it as it is.
+ * It lets go of the pages behind; one that no other sequence holds goes back
+ * to the free stack.  The i-th page given back, sequences in order and their
+ * pages in order (one that several sequences of this call let go: at the last of
+ * them), is free_pages[*free_count_out - 1 - i], so that a trim undoes
+ * fd_page_tables' step.
+ * A sequence that keeps a part of a page lets the page go too if others still hold
+ * it, and gets a copy (an entry of the copy list); if only sequences of this call
+ * that keep a part of it hold it, the last of them keeps the page.  The i-th
+ * copy, sequences in order, takes free_pages[free_count - 1 - i], before pages are given
+ * back.  Where the list, as it was before the call, does not cover in that
+ * order a sequence that ends inside a page with shares > 0, that sequence is
+ * left as it is.
+ *  desc     : n_slots: entries of copy_src and copy_dst, >= batch if shares is given;
+ *             batch*(max_pages_per_seq + 1) < 2^30.
+ *  keep, seqlens, seqlens_out : device int32[batch]; the last two may be the same.
+ *  free_pages : device int32[n_free_max], in and out: pages that find no room in
+ *             it are lost.
+ *  block_table : entries of pages that a copy replaced are written, all others
+ *             left as they are.
+ *  shares   : device int32[n_pages], in and out; NULL: no page is shared (then
+ *             copy_src, copy_dst and copy_count may be NULL).
+ * What is left as it is for lack of a page, a length out of range, a page index outside the pool (the
+ * page is not given back), a page let go more often than it was held, a free count
+ * out of range and a page without room set FD_ERR_DEVICE_BOUNDS in the status word. */
+fd_status fd_page_trim(const fd_page_desc* desc, const int32_t* keep, const int32_t* seqlens,
+                       int32_t* free_pages, const int32_t* free_count, int32_t* block_table,
+                       int32_t* shares, int32_t* seqlens_out, int32_t* free_count_out,
+                       int32_t* copy_src, int32_t* copy_dst, int32_t* copy_count, void* stream);
+
+#define FD_MAX_COMPACT_PAGES (1 << 22)   /* pages of the pool behind n_keep in one fd_page_compact call */
+
+/* Compaction: the pages from n_keep on that the tables hold move to free pages
+ * below n_keep, so that the high end of the pool can be given up.  F: the entries
+ * of the free stack with 0 <= page < n_keep, in their order.  The i-th held page from
+ * n_keep on, ascending, becomes F[f - 1 - i] (f entries) in every table, its shares go
+ * along, and the copy list gets (old, new).  Afterwards the free stack is F
+ * without its last pages, the ones used, written from free_pages[0] on (the
+ * rest of the array is left as it is); pages from n_keep on are in it no more.
+ *  desc     : n_slots: entries of copy_src and copy_dst;
+ *             n_pages - n_keep <= FD_MAX_COMPACT_PAGES.
+ *  n_keep   : 0 <= n_keep <= n_pages.
+ *  seqlens  : device int32[batch].
+ *  shares   : device int32[n_pages], in and out; NULL: no page is shared.
+ * Pages that F or the copy list cannot take stay where they are.  Those, a
+ * length out of range (its table entries are left as they are), a page index
+ * outside the pool and a free count out of range set FD_ERR_DEVICE_BOUNDS in the status word. */
+fd_status fd_page_compact(const fd_page_desc* desc, int32_t n_keep, const int32_t* seqlens,
+                          int32_t* free_pages, const int32_t* free_count, int32_t* block_table,
+                          int32_t* shares, int32_t* free_count_out, int32_t* copy_src,
+                          int32_t* copy_dst, int32_t* copy_count, void* stream);
+
+/* One pool of pages: page P at base + P*page_stride, of it extent[0] x extent[1] rows of
+ * row_bytes bytes, row (i, j) at i*stride[0] + j*stride[1] (bytes): a layer's
+ * K or V cache ([n_kv_heads] x [page_size] rows, any order) or its scales. */
+typedef struct fd_pool {
+    void* base;                 /* device */
+    int64_t page_stride;        /* bytes, > 0 */
+    int64_t stride[2];          /* bytes, >= 0; > 0 where extent > 1 */
+    int32_t extent[2];          /* >= 1 */
+    int32_t row_bytes;          /* >= 1 */
+    int32_t reserved;           /* must be 0 */
+} fd_pool;
+
+/* Copies pages: in every pool page copy_dst[i] becomes what page copy_src[i] is.
+ *  pools      : host fd_pool[n_pools], n_pools >= 0, each with n_pages pages.
+ *  n_pairs    : entries of copy_src and copy_dst (device int32).
+ *  copy_count : device int32[1]: how many of them count, at most n_pairs; NULL: all.
+ * A pair with a negative index, or of a page with itself, is left out; so is one with an
+ * index beyond the pool, which sets FD_ERR_DEVICE_BOUNDS in the status word.  A page
+ * may be the source of many pairs; one that is a destination is in no other pair
+ * (else what it and they get is unspecified). */
+fd_status fd_page_copy(const fd_pool* pools, int32_t n_pools, int32_t n_pages, int32_t n_pairs,
+                       const int32_t* copy_src, const int32_t* copy_dst, const int32_t* copy_count,
+                       void* stream);
 
 #ifdef __cplusplus
 }

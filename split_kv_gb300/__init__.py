@@ -39,6 +39,9 @@ FD_TILE_TOKENS = 128
 FD_STATIC_WORKSPACE_BYTES = 8 << 20
 FD_FLAG_CUDA_CORES = 1
 FD_FLAG_TEST_DROP_FIRST_STAGE = 1 << 16
+FD_NORM_Q, FD_NORM_K = 1, 2
+FD_MAX_TABLE_BATCH = 8192
+FD_MAX_COMPACT_PAGES = 1 << 22
 
 LIB_PATH = _build.LIB_PATH
 
@@ -46,7 +49,8 @@ LIB_PATH = _build.LIB_PATH
 EXPORTS = ("fd_abi_version", "fd_status_string", "fd_num_sms", "fd_plan_splits", "fd_plan",
            "fd_plan_desc", "fd_workspace_size", "fd_decode", "fd_split_states", "fd_combine_states",
            "fd_device_status", "fd_decode_status", "fd_decode_static", "fd_decode_scaled",
-           "fd_cache_store", "fd_page_tables", "fd_prompt", "fd_prompt_workspace_size")
+           "fd_cache_store", "fd_page_tables", "fd_prompt", "fd_prompt_workspace_size", "fd_qkv_rope",
+           "fd_page_fork", "fd_page_trim", "fd_page_compact", "fd_page_copy")
 
 
 class FdDesc(ctypes.Structure):
@@ -118,6 +122,27 @@ class FdPromptDesc(ctypes.Structure):
     ]
 
 
+class FdRopeDesc(ctypes.Structure):
+    """Mirror of ``fd_rope_desc`` (include/fd.h)."""
+    _fields_ = [
+        *((n, ctypes.c_int32) for n in ("n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "dtype", "cache_dtype",
+                                        "w_dtype", "norm", "rot_dim", "interleaved")),
+        *((n, ctypes.c_float) for n in ("eps", "rot_scale", "k_scale", "v_scale")),
+        *((n, ctypes.c_int64) for n in (
+            "q_stride_t", "q_stride_h", "k_src_stride_t", "k_src_stride_h", "v_src_stride_t", "v_src_stride_h",
+            "q_out_stride_t", "q_out_stride_h", "k_out_stride_t", "k_out_stride_h",
+            "k_stride_b", "k_stride_h", "k_stride_t", "v_stride_b", "v_stride_h", "v_stride_t",
+            "q_w_stride_h", "k_w_stride_h", "kv_extent")),
+        *((n, ctypes.c_int32) for n in ("page_size", "batch", "flags", "reserved")),
+    ]
+
+
+class FdPool(ctypes.Structure):
+    """Mirror of ``fd_pool`` (include/fd.h)."""
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("stride", ctypes.c_int64 * 2),
+                ("extent", ctypes.c_int32 * 2), ("row_bytes", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class FdError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = int(status)
@@ -166,6 +191,11 @@ def _load():
             "fd_page_tables": (i32, [ctypes.POINTER(FdPageDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "fd_prompt_workspace_size": (sz, [ctypes.POINTER(FdPromptDesc)]),
             "fd_prompt": (i32, [ctypes.POINTER(FdPromptDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "fd_qkv_rope": (i32, [ctypes.POINTER(FdRopeDesc)] + [vp] * 13),
+            "fd_page_fork": (i32, [ctypes.POINTER(FdPageDesc), i32] + [vp] * 14),
+            "fd_page_trim": (i32, [ctypes.POINTER(FdPageDesc)] + [vp] * 12),
+            "fd_page_compact": (i32, [ctypes.POINTER(FdPageDesc), i32] + [vp] * 10),
+            "fd_page_copy": (i32, [ctypes.POINTER(FdPool), i32, i32, i32, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -242,6 +272,15 @@ def _check_scales(desc, scales: FdKvScales) -> None:
     tokens = page if page > 0 else desc.kv_extent
     if lead < (desc.kv_extent if page > 0 else desc.batch) or heads < desc.n_kv_heads or blocks * scales.block < tokens:
         raise ValueError(f"scales {scales.shape} of {scales.block}-token blocks do not cover the cache")
+
+
+def _ints(name: str, t, n: int) -> None:
+    """t, if it is a tensor, holds n contiguous int32 (addresses and None go unchecked)."""
+    try:
+        if t.element_size() != 4 or t.is_floating_point() or t.nbytes < 4 * n or not t.is_contiguous():
+            raise ValueError(f"{name} must be {n} contiguous int32")
+    except AttributeError:
+        pass
 
 
 def check(status: int, what: str = "") -> int:
@@ -383,6 +422,76 @@ def fd_prompt(desc: FdPromptDesc, q, k, v, cu_q, cu_k, out, lse, workspace=None,
                              _ptr(lse), _ptr(workspace), wb, _stream(stream))
 
 
+def fd_qkv_rope(desc: FdRopeDesc, q, k, v, q_weight, k_weight, inv_freq, positions, slots, q_out, k_out, k_cache,
+                v_cache, stream=None) -> int:
+    """Norms and rotation of a step's queries and keys, and the way of its keys and values into a cache."""
+    n = desc.n_tokens
+    _ints("positions", positions, n)
+    try:
+        if inv_freq is not None and (inv_freq.nbytes < 2 * desc.rot_dim or inv_freq.element_size() != 4 or not inv_freq.is_contiguous()):
+            raise ValueError(f"inv_freq must be {desc.rot_dim // 2} contiguous float32")
+    except AttributeError:
+        pass
+    try:
+        if slots is not None and (slots.element_size() != 8 or slots.nbytes < 8 * n or not slots.is_contiguous()):
+            raise ValueError(f"slots must be {n} contiguous int64")
+    except AttributeError:
+        pass
+    return _load().fd_qkv_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                               _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache),
+                               _stream(stream))
+
+
+def _check_page_lists(desc, seqlens, free_pages, block_table, shares, seqlens_out, copy_src, copy_dst) -> None:
+    _ints("seqlens", seqlens, desc.batch)
+    _ints("free_pages", free_pages, desc.n_free_max)
+    _ints("block_table", block_table, desc.batch * desc.max_pages_per_seq)
+    _ints("shares", shares, desc.n_pages)
+    _ints("seqlens_out", seqlens_out, desc.batch)
+    _ints("copy_src", copy_src, desc.n_slots)
+    _ints("copy_dst", copy_dst, desc.n_slots)
+
+
+def fd_page_fork(desc: FdPageDesc, parents, children, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out,
+                 free_count_out, copy_src, copy_dst, copy_count, n_forks: int | None = None, stream=None) -> int:
+    """Sequences children[i] that share the pages of parents[i]'s first keep[i] tokens (None: of all)."""
+    n = parents.numel() if n_forks is None else int(n_forks)
+    for name, t in (("parents", parents), ("children", children), ("keep", keep)):
+        _ints(name, t, n)
+    _check_page_lists(desc, seqlens, free_pages, block_table, shares, seqlens_out, copy_src, copy_dst)
+    return _load().fd_page_fork(ctypes.byref(desc), n, _ptr(parents), _ptr(children), _ptr(keep), _ptr(seqlens),
+                                _ptr(free_pages), _ptr(free_count), _ptr(block_table), _ptr(shares), _ptr(seqlens_out),
+                                _ptr(free_count_out), _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _stream(stream))
+
+
+def fd_page_trim(desc: FdPageDesc, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out, free_count_out,
+                 copy_src=None, copy_dst=None, copy_count=None, stream=None) -> int:
+    """Sequences cut to their first keep[b] tokens; pages that nobody holds any more go back to the free stack."""
+    _ints("keep", keep, desc.batch)
+    _check_page_lists(desc, seqlens, free_pages, block_table, shares, seqlens_out, copy_src, copy_dst)
+    return _load().fd_page_trim(ctypes.byref(desc), _ptr(keep), _ptr(seqlens), _ptr(free_pages), _ptr(free_count),
+                                _ptr(block_table), _ptr(shares), _ptr(seqlens_out), _ptr(free_count_out), _ptr(copy_src),
+                                _ptr(copy_dst), _ptr(copy_count), _stream(stream))
+
+
+def fd_page_compact(desc: FdPageDesc, n_keep: int, seqlens, free_pages, free_count, block_table, shares, free_count_out,
+                    copy_src, copy_dst, copy_count, stream=None) -> int:
+    """Held pages from n_keep on renamed to free pages below it, for the high end of a pool to be given up."""
+    _check_page_lists(desc, seqlens, free_pages, block_table, shares, None, copy_src, copy_dst)
+    return _load().fd_page_compact(ctypes.byref(desc), int(n_keep), _ptr(seqlens), _ptr(free_pages), _ptr(free_count),
+                                   _ptr(block_table), _ptr(shares), _ptr(free_count_out), _ptr(copy_src), _ptr(copy_dst),
+                                   _ptr(copy_count), _stream(stream))
+
+
+def fd_page_copy(pools, copy_src, copy_dst, copy_count=None, n_pairs: int | None = None, stream=None) -> int:
+    """Page copy_dst[i] of every pool (make_pools) becomes what page copy_src[i] is."""
+    n = copy_src.numel() if n_pairs is None else int(n_pairs)
+    _ints("copy_src", copy_src, n)
+    _ints("copy_dst", copy_dst, n)
+    return _load().fd_page_copy(pools, len(pools), pools.n_pages, n, _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count),
+                                _stream(stream))
+
+
 def fd_device_status(stream=None, clear: bool = True) -> int:
     return int(_load().fd_device_status(_stream(stream), 1 if clear else 0))
 
@@ -491,21 +600,129 @@ def make_store_desc(k, v, k_cache, v_cache, *, page_size: int = 0) -> FdStoreDes
     return d
 
 
-def make_page_desc(block_table, free_pages, slots, *, page_size: int, n_pages: int) -> FdPageDesc:
+def make_page_desc(block_table, free_pages, slots, *, page_size: int, n_pages: int, copies=None) -> FdPageDesc:
     """Descriptor for a table [B, max_pages_per_seq] (contiguous int32), the free stack (int32)
-    and the slot map (int64)."""
+    and the slot map (int64) of fd_page_tables, or, with slots None, the copy list's
+    arrays (copies: one of them, int32; None: no list) of fd_page_fork, _trim and _compact."""
     import torch
     if block_table.dim() != 2 or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous [B, max_pages_per_seq] tensor")
     if block_table.dtype != torch.int32 or free_pages.dtype != torch.int32 or not free_pages.is_contiguous():
         raise ValueError("block_table and free_pages must be contiguous int32 tensors")
-    if slots.dtype != torch.int64 or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous int64 tensor")
+    if slots is not None:
+        if slots.dtype != torch.int64 or not slots.is_contiguous():
+            raise ValueError("slots must be a contiguous int64 tensor")
+        if copies is not None:
+            raise ValueError("a descriptor has a slot map or a copy list")
+    elif copies is not None and (copies.dtype != torch.int32 or not copies.is_contiguous()):
+        raise ValueError("copies must be a contiguous int32 tensor")
     d = FdPageDesc()
     d.batch, d.max_pages_per_seq = block_table.shape
     d.page_size, d.n_pages = int(page_size), int(n_pages)
-    d.n_free_max, d.n_slots = free_pages.numel(), slots.numel()
+    d.n_free_max = free_pages.numel()
+    d.n_slots = slots.numel() if slots is not None else copies.numel() if copies is not None else 0
     return d
+
+
+def make_rope_desc(q, k, v=None, *, q_out=None, k_out=None, k_cache=None, v_cache=None, page_size: int = 0, q_weight=None,
+                   k_weight=None, norm_q: bool = True, norm_k: bool = True, rot_dim: int = 128, interleaved: bool = False,
+                   eps: float = 1e-6, rot_scale: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0) -> FdRopeDesc:
+    """Descriptor for a step's heads q [n, Hq, D], k and v [n, Hkv, D] (16-bit, any strides with
+    whole 16-byte rows; q or k may be None), rows out q_out and k_out of their shapes, caches
+    [P, Hkv, page, D] (paged) or [B, Hkv, T, D] (page_size 0) of their type or float8_e4m3fn,
+    and weights [D] or [heads, D]."""
+    d = FdRopeDesc()
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    d.n_tokens, _, d.head_dim = x.shape
+    d.dtype = _dtype_code(x.dtype)
+    if (k_cache is None) != (v_cache is None) or (k_cache is not None and (v is None or k is None)):
+        raise ValueError("a cache takes k, v, k_cache and v_cache")
+    if q is not None and q_out is None or k is not None and k_out is None and k_cache is None:
+        raise ValueError("q needs q_out, k needs k_out or caches")
+    for name, t, like in (("q", q, None), ("k", k, None), ("v", v if k_cache is not None else None, k), ("q_out", q_out, q),
+                          ("k_out", k_out, k)):
+        if t is None:
+            continue
+        if t.dim() != 3 or t.shape[0] != d.n_tokens or t.shape[2] != d.head_dim or t.dtype != x.dtype or t.stride(2) != 1:
+            raise ValueError(f"{name} must be [{d.n_tokens}, heads, {d.head_dim}] of one 16-bit type, the head dimension contiguous")
+        if name not in "qk" and (like is None or t.shape != like.shape):
+            raise ValueError(f"{name} must have the shape of its rows")
+    d.n_q_heads = 0 if q is None else q.shape[1]
+    d.n_kv_heads = 0 if k is None else k.shape[1]
+    if q is not None:
+        d.q_stride_t, d.q_stride_h = q.stride()[:2]
+        d.q_out_stride_t, d.q_out_stride_h = q_out.stride()[:2]
+    if k is not None:
+        d.k_src_stride_t, d.k_src_stride_h = k.stride()[:2]
+        if k_out is not None:
+            d.k_out_stride_t, d.k_out_stride_h = k_out.stride()[:2]
+    d.cache_dtype = d.dtype
+    if k_cache is not None:
+        d.v_src_stride_t, d.v_src_stride_h = v.stride()[:2]
+        if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+            raise ValueError("k_cache and v_cache must have the same shape and type")
+        if k_cache.dim() != 4 or k_cache.shape[1] != d.n_kv_heads or k_cache.shape[3] != d.head_dim:
+            raise ValueError("the caches must be [pages or sequences, Hkv, tokens, D]")
+        if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+            raise ValueError("the head dimension must be contiguous")
+        if page_size and k_cache.shape[2] != page_size:
+            raise ValueError("a paged cache's third dimension is its page size")
+        d.cache_dtype = _dtype_code(k_cache.dtype)
+        d.k_stride_b, d.k_stride_h, d.k_stride_t = k_cache.stride()[:3]
+        d.v_stride_b, d.v_stride_h, d.v_stride_t = v_cache.stride()[:3]
+        d.page_size = int(page_size)
+        d.kv_extent = k_cache.shape[0] if page_size else k_cache.shape[2]
+        d.batch = k_cache.shape[0]
+    d.norm = (FD_NORM_Q if norm_q and q is not None else 0) | (FD_NORM_K if norm_k and k is not None else 0)
+    d.w_dtype = FD_F32
+    types = set()
+    for name, w, heads in (("q_weight", q_weight, d.n_q_heads), ("k_weight", k_weight, d.n_kv_heads)):
+        if w is None:
+            continue
+        if w.shape[-1] != d.head_dim or w.dim() > 2 or w.stride(-1) != 1 or (w.dim() == 2 and w.shape[0] != heads):
+            raise ValueError(f"{name} must be [D] or [heads, D], the last dimension contiguous")
+        types.add(w.dtype)
+        if w.dim() == 2 and heads > 1:
+            setattr(d, name[0] + "_w_stride_h", w.stride(0))
+        d.w_dtype = _dtype_code(w.dtype)
+    if len(types) > 1:
+        raise ValueError("q_weight and k_weight must have one type")
+    d.rot_dim, d.interleaved = int(rot_dim), int(bool(interleaved))
+    d.eps, d.rot_scale, d.k_scale, d.v_scale = float(eps), float(rot_scale), float(k_scale), float(v_scale)
+    d.flags = d.reserved = 0
+    return d
+
+
+def make_pools(tensors):
+    """Pools of fd_page_copy: tensors [P, ...] of up to four dimensions with one number of pages
+    (a layer's K or V cache [P, Hkv, page, D] in any order of storage, its scales [P, Hkv,
+    page / block]).  The tensors are kept alive by the returned array."""
+    tensors = list(tensors)
+    pools = (FdPool * len(tensors))()
+    pages = {t.shape[0] for t in tensors}
+    if len(pages) > 1 or 0 in pages:
+        raise ValueError("the pools must have one number of pages")
+    for x, t in zip(pools, tensors):
+        size = t.element_size()
+        inner = [(n, st * size) for n, st in zip(t.shape[1:], t.stride()[1:]) if n != 1]
+        if 0 in t.shape or len(inner) > 3:
+            raise ValueError("a pool is a tensor [pages, ...] of up to four dimensions, none of them empty")
+        x.row_bytes = size
+        if inner and inner[-1][1] == size:
+            x.row_bytes *= inner.pop()[0]
+        if len(inner) > 2:
+            raise ValueError("a pool's last dimension must be contiguous")
+        inner = [(1, 0)] * (2 - len(inner)) + inner
+        x.base = t.data_ptr()
+        x.page_stride = t.stride(0) * size if t.shape[0] > 1 else max(1, t.stride(0)) * size
+        for i, (n, st) in enumerate(inner):
+            x.extent[i], x.stride[i] = n, st
+        x.reserved = 0
+    pools.n_pages = pages.pop() if pages else 1
+    pools._keep = tensors
+    return pools
 
 
 def make_prompt_desc(q, k, v, *, batch: int, causal: bool = True, max_q: int = 0, max_k: int = 0,

@@ -13,7 +13,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libfd.so")
 ROOT = os.path.dirname(HERE)
 
 CU_SOURCES = ["fd_split.cu", "fd_combine.cu", "fd_tables.cu", "fd_store.cu", "fd_prompt.cu",
-              "fd_api.cu"]
+              "fd_rope.cu", "fd_pages.cu", "fd_copy.cu", "fd_api.cu"]
 CPP_SOURCES = ["fd_plan.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -406,6 +406,142 @@ fd_status make_rows_map(CUtensorMap* map, bool bf16, const void* base, int64_t r
     return r == CUDA_SUCCESS ? FD_OK : FD_ERR_INVALID_ARG;
 }
 
+// What fd_page_fork, fd_page_trim and fd_page_compact ask of a descriptor.
+fd_status check_pages(const fd_page_desc* d) {
+    if (d == nullptr || d->batch < 0 || d->page_size < 1 || (d->page_size & (d->page_size - 1)) != 0 ||
+        d->page_size > (1 << 20) || d->max_pages_per_seq < 1 || d->n_pages < 1 || d->n_free_max < 0 || d->n_slots < 0)
+        return FD_ERR_INVALID_ARG;
+    if (d->page_size < 8 || d->batch > FD_MAX_TABLE_BATCH) return FD_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(d->max_pages_per_seq) * d->page_size > INT32_MAX) return FD_ERR_INVALID_ARG;
+    return FD_OK;
+}
+
+// Addresses of int32 arrays; `needed` ones may not be null.
+bool ints_ok(std::initializer_list<const void*> needed, std::initializer_list<const void*> may_be_null) {
+    for (const void* x : needed)
+        if (x == nullptr || !aligned_to(x, 4)) return false;
+    for (const void* x : may_be_null)
+        if (!aligned_to(x, 4)) return false;
+    return true;
+}
+
+fdk::PagePlanParams page_plan(const fd_page_desc* d) {
+    fdk::PagePlanParams p = {};
+    p.batch = d->batch;
+    p.page_shift = log2_of(d->page_size);
+    p.max_pages = d->max_pages_per_seq;
+    p.n_pages = d->n_pages;
+    p.n_free_max = d->n_free_max;
+    p.n_copies = d->n_slots;
+    return p;
+}
+
+fd_status check_rope(const fd_rope_desc* d, bool cached, bool k_rows) {
+    if (d == nullptr || d->n_tokens < 0 || d->n_q_heads < 0 || d->n_kv_heads < 0 || d->n_q_heads + static_cast<int64_t>(d->n_kv_heads) < 1 ||
+        d->head_dim < 1)
+        return FD_ERR_INVALID_ARG;
+    if (d->flags != 0 || d->reserved != 0 || (d->interleaved != 0 && d->interleaved != 1) ||
+        (d->norm & ~(FD_NORM_Q | FD_NORM_K)) != 0)
+        return FD_ERR_INVALID_ARG;
+    if (d->dtype != FD_F16 && d->dtype != FD_BF16)
+        return d->dtype == FD_F32 || d->dtype == FD_E4M3 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (d->norm != 0 && d->w_dtype != FD_F16 && d->w_dtype != FD_BF16 && d->w_dtype != FD_F32)
+        return d->w_dtype == FD_E4M3 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (d->head_dim != kHeadDim) return FD_ERR_UNSUPPORTED;
+    if (d->rot_dim < 0 || d->rot_dim > kHeadDim || d->rot_dim % 2 != 0) return FD_ERR_INVALID_ARG;
+    if (d->rot_dim % 16 != 0 || d->n_q_heads > 65535 || d->n_kv_heads > 65535) return FD_ERR_UNSUPPORTED;
+    if (!(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->rot_scale)) return FD_ERR_INVALID_ARG;
+    for (const int64_t s : {d->q_stride_t, d->q_stride_h, d->k_src_stride_t, d->k_src_stride_h, d->v_src_stride_t,
+                            d->v_src_stride_h, d->q_out_stride_t, d->q_out_stride_h, d->k_out_stride_t,
+                            d->k_out_stride_h, d->q_w_stride_h, d->k_w_stride_h})
+        if (!stride_ok(s)) return FD_ERR_INVALID_ARG;
+    // what is written has a place of its own
+    if (d->n_q_heads > 0 && ((d->q_out_stride_t < kHeadDim && d->n_tokens > 1) || (d->q_out_stride_h < kHeadDim && d->n_q_heads > 1)))
+        return FD_ERR_INVALID_ARG;
+    if (k_rows && ((d->k_out_stride_t < kHeadDim && d->n_tokens > 1) || (d->k_out_stride_h < kHeadDim && d->n_kv_heads > 1)))
+        return FD_ERR_INVALID_ARG;
+    if (!cached) return FD_OK;
+    if (d->n_kv_heads < 1) return FD_ERR_INVALID_ARG;
+    const bool fp8 = d->cache_dtype == FD_E4M3;
+    if (!fp8 && d->cache_dtype != d->dtype)
+        return d->cache_dtype == FD_F16 || d->cache_dtype == FD_BF16 || d->cache_dtype == FD_F32 ? FD_ERR_UNSUPPORTED
+                                                                                               : FD_ERR_INVALID_ARG;
+    if (fp8)
+        for (const float s : {d->k_scale, d->v_scale})
+            if (!(s > 0.f) || !std::isnormal(s)) return FD_ERR_INVALID_ARG;
+    if (d->page_size < 0) return FD_ERR_INVALID_ARG;
+    if (d->page_size > 0) {
+        if ((d->page_size & (d->page_size - 1)) != 0 || d->page_size > (1 << 20)) return FD_ERR_INVALID_ARG;
+        if (d->page_size < 8) return FD_ERR_UNSUPPORTED;
+    } else if (d->batch < 1) {
+        return FD_ERR_INVALID_ARG;
+    }
+    if (d->kv_extent < 1 || d->kv_extent > INT32_MAX) return FD_ERR_INVALID_ARG;
+    const int es = fp8 ? 1 : 2;
+    for (const int64_t s : {d->k_stride_b, d->k_stride_h, d->k_stride_t, d->v_stride_b, d->v_stride_h, d->v_stride_t})
+        if (!stride_ok(s, es)) return FD_ERR_INVALID_ARG;
+    if (d->k_stride_t < kHeadDim || d->v_stride_t < kHeadDim) return FD_ERR_INVALID_ARG;
+    const int64_t lead = d->page_size > 0 ? d->kv_extent : d->batch;
+    if (shared_rows(d->k_stride_b, lead) || shared_rows(d->v_stride_b, lead) || shared_rows(d->k_stride_h, d->n_kv_heads) ||
+        shared_rows(d->v_stride_h, d->n_kv_heads))
+        return FD_ERR_INVALID_ARG;
+    return FD_OK;
+}
+
+// A pool with its dimensions joined where one goes on in the next, and the
+// largest unit that divides all it is addressed by.
+struct PoolShape {
+    int64_t page_stride, stride0, stride1;
+    int64_t extent0, extent1, row_bytes;
+    bool operator==(const PoolShape& o) const {
+        return page_stride == o.page_stride && stride0 == o.stride0 && stride1 == o.stride1 && extent0 == o.extent0 &&
+               extent1 == o.extent1 && row_bytes == o.row_bytes;
+    }
+};
+
+PoolShape pool_shape(const fd_pool& x) {
+    PoolShape s = {x.page_stride, x.stride[0], x.stride[1], x.extent[0], x.extent[1], x.row_bytes};
+    // rows in the order of their addresses (a copy does not care which index is the outer one)
+    if (s.extent1 == 1 || (s.extent0 > 1 && s.stride0 < s.stride1)) {
+        std::swap(s.stride0, s.stride1);
+        std::swap(s.extent0, s.extent1);
+    }
+    for (int i = 0; i < 2; ++i)
+        if (s.extent1 == 1 || s.stride1 == s.row_bytes) {   // the inner rows lie end to end: one row
+            s.row_bytes *= s.extent1;
+            s.stride1 = s.stride0;
+            s.extent1 = s.extent0;
+            s.stride0 = 0;
+            s.extent0 = 1;
+        }
+    if (s.extent0 == 1) s.stride0 = 0;
+    if (s.extent1 == 1) s.stride1 = 0;
+    return s;
+}
+
+int pool_unit(const PoolShape& s, const void* base) {
+    const uint64_t bits = static_cast<uint64_t>(s.page_stride) | static_cast<uint64_t>(s.stride0) |
+                          static_cast<uint64_t>(s.stride1) | static_cast<uint64_t>(s.row_bytes) |
+                          reinterpret_cast<uintptr_t>(base);
+    int unit = 16;
+    while ((bits & static_cast<uint64_t>(unit - 1)) != 0) unit /= 2;
+    return unit;
+}
+
+fd_status check_pool(const fd_pool& x, int32_t n_pages) {
+    if (x.base == nullptr || x.reserved != 0 || x.row_bytes < 1) return FD_ERR_INVALID_ARG;
+    int64_t last = x.row_bytes;             // bytes from a page's first to behind its last
+    for (int i = 0; i < 2; ++i) {
+        if (x.extent[i] < 1 || x.stride[i] < 0 || x.stride[i] >= (int64_t(1) << 40)) return FD_ERR_INVALID_ARG;
+        if (x.extent[i] > 1 && x.stride[i] < x.row_bytes) return FD_ERR_INVALID_ARG;   // rows on top of each other
+        last += static_cast<int64_t>(x.extent[i] - 1) * x.stride[i];
+        if (last > (int64_t(1) << 42)) return FD_ERR_INVALID_ARG;
+    }
+    if (x.page_stride < 1 || x.page_stride >= (int64_t(1) << 40)) return FD_ERR_INVALID_ARG;
+    if (n_pages > 1 && x.page_stride < x.row_bytes) return FD_ERR_INVALID_ARG;
+    return FD_OK;
+}
+
 // ---- fixed workspace for fd_decode_static (callers that cannot allocate)
 // The split states of fd_decode_static live here instead of in a caller
 // buffer.  Every device that loads the library holds this array until exit.
@@ -672,6 +808,207 @@ fd_status fd_page_tables(const fd_page_desc* d, const int32_t* seqlens, const in
     p.n_free_max = d->n_free_max;
     p.n_slots = d->n_slots;
     return fdk::launch_page_tables(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_qkv_rope(const fd_rope_desc* d, const void* q, const void* k, const void* v, const void* q_weight,
+                      const void* k_weight, const float* inv_freq, const int32_t* positions, const int64_t* slots,
+                      void* q_out, void* k_out, void* k_cache, void* v_cache, void* stream) {
+    if ((k_cache == nullptr) != (v_cache == nullptr)) return FD_ERR_INVALID_ARG;
+    const bool cached = k_cache != nullptr;
+    const fd_status st = check_rope(d, cached, k_out != nullptr);
+    if (st != FD_OK) return st;
+    if (d->n_tokens == 0) return FD_OK;   // (an empty tensor's address is null)
+    if (positions == nullptr || (d->rot_dim > 0 && inv_freq == nullptr) || (d->n_q_heads > 0 && (q == nullptr || q_out == nullptr)) ||
+        (d->n_kv_heads > 0 && (k == nullptr || (k_out == nullptr && !cached))) || (cached && (v == nullptr || slots == nullptr)))
+        return FD_ERR_INVALID_ARG;
+    for (const void* x : {q, k, v, q_weight, k_weight, const_cast<const void*>(q_out), const_cast<const void*>(k_out),
+                          const_cast<const void*>(k_cache), const_cast<const void*>(v_cache)})
+        if (!aligned16(x)) return FD_ERR_INVALID_ARG;
+    if (!aligned_to(positions, 4) || !aligned_to(inv_freq, 4) || !aligned_to(slots, 8)) return FD_ERR_INVALID_ARG;
+    // in place: with the input's strides
+    if (q != nullptr && q == q_out && (d->q_stride_t != d->q_out_stride_t || d->q_stride_h != d->q_out_stride_h)) return FD_ERR_INVALID_ARG;
+    if (k != nullptr && k == k_out && (d->k_src_stride_t != d->k_out_stride_t || d->k_src_stride_h != d->k_out_stride_h))
+        return FD_ERR_INVALID_ARG;
+    fdk::RopeParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.q_w = q_weight;
+    p.k_w = k_weight;
+    p.inv_freq = inv_freq;
+    p.positions = positions;
+    p.slots = slots;
+    p.q_t = d->q_stride_t;
+    p.q_h = d->q_stride_h;
+    p.k_t = d->k_src_stride_t;
+    p.k_h = d->k_src_stride_h;
+    p.v_t = d->v_src_stride_t;
+    p.v_h = d->v_src_stride_h;
+    p.qo_t = d->q_out_stride_t;
+    p.qo_h = d->q_out_stride_h;
+    p.ko_t = d->k_out_stride_t;
+    p.ko_h = d->k_out_stride_h;
+    p.kc_b = d->k_stride_b;
+    p.kc_h = d->k_stride_h;
+    p.kc_t = d->k_stride_t;
+    p.vc_b = d->v_stride_b;
+    p.vc_h = d->v_stride_h;
+    p.vc_t = d->v_stride_t;
+    p.qw_h = d->q_w_stride_h;
+    p.kw_h = d->k_w_stride_h;
+    const bool fp8 = cached && d->cache_dtype == FD_E4M3;
+    if (cached) {
+        const bool paged = d->page_size > 0;
+        p.row_tokens = paged ? d->page_size : static_cast<int32_t>(d->kv_extent);
+        p.n_slots = (paged ? d->kv_extent : static_cast<int64_t>(d->batch)) * p.row_tokens;
+        p.row_shift = paged ? log2_of(d->page_size) : -1;
+    }
+    p.n_tokens = d->n_tokens;
+    p.n_q_heads = d->n_q_heads;
+    p.n_kv_heads = d->n_kv_heads;
+    p.rot_dim = d->rot_dim;
+    p.norm = d->norm;
+    p.w_dtype = d->w_dtype == FD_F16 ? 0 : d->w_dtype == FD_BF16 ? 1 : 2;
+    p.eps = d->eps;
+    p.rot_scale = d->rot_scale;
+    p.k_inv = fp8 ? 1.f / d->k_scale : 1.f;
+    p.v_inv = fp8 ? 1.f / d->v_scale : 1.f;
+    return fdk::launch_rope(p, d->dtype == FD_BF16, d->interleaved != 0, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FD_OK
+               : FD_ERR_CUDA;
+}
+
+fd_status fd_page_fork(const fd_page_desc* d, int32_t n_forks, const int32_t* parents, const int32_t* children,
+                       const int32_t* keep, const int32_t* seqlens, const int32_t* free_pages, const int32_t* free_count,
+                       int32_t* block_table, int32_t* shares, int32_t* seqlens_out, int32_t* free_count_out,
+                       int32_t* copy_src, int32_t* copy_dst, int32_t* copy_count, void* stream) {
+    const fd_status st = check_pages(d);
+    if (st != FD_OK) return st;
+    if (n_forks < 0 || d->n_slots < n_forks) return FD_ERR_INVALID_ARG;
+    if (n_forks > FD_MAX_TABLE_BATCH) return FD_ERR_UNSUPPORTED;
+    if (!ints_ok({free_count, free_count_out, shares, copy_count},
+                 {parents, children, keep, seqlens, free_pages, block_table, seqlens_out, copy_src, copy_dst}))
+        return FD_ERR_INVALID_ARG;
+    if ((n_forks > 0 && (parents == nullptr || children == nullptr || copy_src == nullptr || copy_dst == nullptr)) ||
+        (d->batch > 0 && (seqlens == nullptr || block_table == nullptr || seqlens_out == nullptr)) ||
+        (d->n_free_max > 0 && free_pages == nullptr))
+        return FD_ERR_INVALID_ARG;
+    fdk::PagePlanParams p = page_plan(d);
+    p.n_forks = n_forks;
+    p.parents = parents;
+    p.children = children;
+    p.keep = keep;
+    p.seqlens = seqlens;
+    p.free_in = free_pages;
+    p.free_count = free_count;
+    p.block_table = block_table;
+    p.shares = shares;
+    p.seqlens_out = seqlens_out;
+    p.free_count_out = free_count_out;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    p.copy_count = copy_count;
+    return fdk::launch_page_fork(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_page_trim(const fd_page_desc* d, const int32_t* keep, const int32_t* seqlens, int32_t* free_pages,
+                       const int32_t* free_count, int32_t* block_table, int32_t* shares, int32_t* seqlens_out,
+                       int32_t* free_count_out, int32_t* copy_src, int32_t* copy_dst, int32_t* copy_count, void* stream) {
+    const fd_status st = check_pages(d);
+    if (st != FD_OK) return st;
+    if (static_cast<int64_t>(d->batch) * (static_cast<int64_t>(d->max_pages_per_seq) + 1) >= (int64_t(1) << 30)) return FD_ERR_UNSUPPORTED;
+    if (shares != nullptr && d->n_slots < d->batch) return FD_ERR_INVALID_ARG;
+    if (!ints_ok({free_count, free_count_out}, {keep, seqlens, free_pages, block_table, shares, seqlens_out, copy_src, copy_dst, copy_count}))
+        return FD_ERR_INVALID_ARG;
+    if ((d->batch > 0 && (keep == nullptr || seqlens == nullptr || block_table == nullptr || seqlens_out == nullptr)) ||
+        (d->n_free_max > 0 && free_pages == nullptr) ||
+        (shares != nullptr && (copy_count == nullptr || (d->batch > 0 && (copy_src == nullptr || copy_dst == nullptr)))))
+        return FD_ERR_INVALID_ARG;
+    fdk::PagePlanParams p = page_plan(d);
+    p.keep = keep;
+    p.seqlens = seqlens;
+    p.free_in = free_pages;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.block_table = block_table;
+    p.shares = shares;
+    p.seqlens_out = seqlens_out;
+    p.free_count_out = free_count_out;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    p.copy_count = copy_count;
+    return fdk::launch_page_trim(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_page_compact(const fd_page_desc* d, int32_t n_keep, const int32_t* seqlens, int32_t* free_pages,
+                          const int32_t* free_count, int32_t* block_table, int32_t* shares, int32_t* free_count_out,
+                          int32_t* copy_src, int32_t* copy_dst, int32_t* copy_count, void* stream) {
+    const fd_status st = check_pages(d);
+    if (st != FD_OK) return st;
+    if (n_keep < 0 || n_keep > d->n_pages) return FD_ERR_INVALID_ARG;
+    if (d->n_pages - n_keep > FD_MAX_COMPACT_PAGES) return FD_ERR_UNSUPPORTED;
+    if (!ints_ok({free_count, free_count_out, copy_count}, {seqlens, free_pages, block_table, shares, copy_src, copy_dst}))
+        return FD_ERR_INVALID_ARG;
+    if ((d->batch > 0 && (seqlens == nullptr || block_table == nullptr)) || (d->n_free_max > 0 && free_pages == nullptr) ||
+        (d->n_slots > 0 && (copy_src == nullptr || copy_dst == nullptr)))
+        return FD_ERR_INVALID_ARG;
+    fdk::PagePlanParams p = page_plan(d);
+    p.n_keep = n_keep;
+    p.seqlens = seqlens;
+    p.free_in = free_pages;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.block_table = block_table;
+    p.shares = shares;
+    p.free_count_out = free_count_out;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    p.copy_count = copy_count;
+    return fdk::launch_page_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_page_copy(const fd_pool* pools, int32_t n_pools, int32_t n_pages, int32_t n_pairs, const int32_t* copy_src,
+                       const int32_t* copy_dst, const int32_t* copy_count, void* stream) {
+    if (n_pools < 0 || n_pages < 1 || n_pairs < 0 || (n_pools > 0 && pools == nullptr)) return FD_ERR_INVALID_ARG;
+    for (int i = 0; i < n_pools; ++i) {
+        const fd_status st = check_pool(pools[i], n_pages);
+        if (st != FD_OK) return st;
+    }
+    if (!ints_ok({}, {copy_src, copy_dst, copy_count})) return FD_ERR_INVALID_ARG;
+    if (n_pools == 0 || n_pairs == 0) return FD_OK;   // (an empty tensor's address is null)
+    if (copy_src == nullptr || copy_dst == nullptr) return FD_ERR_INVALID_ARG;
+    // one launch for the pools of one shape that follow each other
+    int first = 0;
+    while (first < n_pools) {
+        const PoolShape s = pool_shape(pools[first]);
+        fdk::CopyParams p = {};
+        p.page_stride = s.page_stride;
+        p.stride0 = s.stride0;
+        p.stride1 = s.stride1;
+        p.extent0 = static_cast<int32_t>(s.extent0);
+        p.extent1 = static_cast<int32_t>(s.extent1);
+        p.row_bytes = s.row_bytes;
+        p.unit = 16;
+        int n = 0;
+        for (; n < fdk::kPoolsPerLaunch && first + n < n_pools; ++n) {
+            if (n > 0 && !(pool_shape(pools[first + n]) == s)) break;
+            p.base[n] = static_cast<char*>(pools[first + n].base);
+            p.unit = std::min(p.unit, pool_unit(s, p.base[n]));
+        }
+        p.n_pools = n;
+        p.n_pages = n_pages;
+        p.n_pairs = n_pairs;
+        p.src = copy_src;
+        p.dst = copy_dst;
+        p.count = copy_count;
+        if (fdk::launch_page_copy(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FD_ERR_CUDA;
+        first += n;
+    }
+    return FD_OK;
 }
 
 size_t fd_prompt_workspace_size(const fd_prompt_desc* desc) {

@@ -208,11 +208,75 @@ struct PromptParams {
 cudaError_t launch_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           const PromptParams& p, bool bf16, int64_t tiles, cudaStream_t stream);
 
+// ---- norms and rotation into a cache; forks, trims, compaction and copies of pages
+
+struct RopeParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_out;                    // or null
+    void* k_cache;                  // or null, and v_cache with it
+    void* v_cache;
+    const void* q_w;                // or null
+    const void* k_w;
+    const float* inv_freq;
+    const int32_t* positions;
+    const int64_t* slots;
+    int64_t q_t, q_h, k_t, k_h, v_t, v_h, qo_t, qo_h, ko_t, ko_h;   // elements
+    int64_t kc_b, kc_h, kc_t, vc_b, vc_h, vc_t, qw_h, kw_h;
+    int64_t n_slots;                // places in the caches
+    int32_t row_tokens;             // tokens per page, or per sequence of a contiguous cache
+    int32_t row_shift;              // log2(row_tokens) of pages; -1 for a contiguous cache
+    int32_t n_tokens, n_q_heads, n_kv_heads;
+    int32_t rot_dim, norm, w_dtype; // FD_NORM_* bits; 0 f16, 1 bf16, 2 f32
+    float eps, rot_scale, k_inv, v_inv;
+};
+cudaError_t launch_rope(const RopeParams& p, bool bf16, bool interleaved, bool fp8_cache, cudaStream_t stream);
+
+struct PagePlanParams {             // of forks, trims and compaction
+    const int32_t* parents;         // forks
+    const int32_t* children;
+    const int32_t* keep;            // forks: or null; trims
+    const int32_t* seqlens;
+    const int32_t* free_in;         // == free_pages where those are written
+    int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* block_table;
+    int32_t* shares;                // or null (not forks)
+    int32_t* seqlens_out;
+    int32_t* free_count_out;
+    int32_t* copy_src;
+    int32_t* copy_dst;
+    int32_t* copy_count;
+    int32_t batch, page_shift, max_pages, n_pages, n_free_max, n_copies, n_forks, n_keep;
+};
+cudaError_t launch_page_fork(const PagePlanParams& p, cudaStream_t stream);
+cudaError_t launch_page_trim(const PagePlanParams& p, cudaStream_t stream);
+cudaError_t launch_page_compact(const PagePlanParams& p, cudaStream_t stream);
+
+constexpr int kPoolsPerLaunch = 64;
+struct CopyParams {                 // pools of one geometry; bytes
+    char* base[kPoolsPerLaunch];
+    int64_t page_stride, stride0, stride1;
+    int64_t row_bytes;
+    int32_t extent0, extent1;
+    int32_t unit;                   // bytes that divide addresses, strides and row_bytes: 1, 2, 4, 8 or 16
+    int32_t n_pools, n_pages, n_pairs;
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* count;           // or null
+};
+cudaError_t launch_page_copy(const CopyParams& p, cudaStream_t stream);
+
 // The status words.  Each file that raises bits owns one (device symbols do
 // not cross files here); read_status joins them.
 cudaError_t status_word_tables(unsigned** word);
 cudaError_t status_word_store(unsigned** word);
 cudaError_t status_word_prompt(unsigned** word);
+cudaError_t status_word_rope(unsigned** word);
+cudaError_t status_word_pages(unsigned** word);
+cudaError_t status_word_copy(unsigned** word);
 
 // Waits for `stream`, then reads (and with `clear` resets) every status word (fd_split.cu).
 cudaError_t read_status(unsigned* value, cudaStream_t stream, bool clear);

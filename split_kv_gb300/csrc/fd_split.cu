@@ -2362,8 +2362,14 @@ cudaError_t launch_split(const CUtensorMap& tmK, const CUtensorMap& tmV, const S
 
 // Joins the status words into this file's (or, to clear, resets them all).
 __device__ unsigned int g_joined = 0;
-__global__ void fd_status_kernel(unsigned* a, unsigned* b, unsigned* c, bool clear) {
-    const unsigned v = atomicExch(a, 0u) | atomicExch(b, 0u) | atomicExch(c, 0u);
+constexpr int kStatusWords = 6;         // of the other files
+struct StatusWords {
+    unsigned* word[kStatusWords];
+};
+__global__ void fd_status_kernel(const StatusWords s, bool clear) {
+    unsigned v = 0;
+#pragma unroll
+    for (int i = 0; i < kStatusWords; ++i) v |= atomicExch(s.word[i], 0u);
     g_joined = v | (clear ? atomicExch(&g_fd_status, 0u) : atomicOr(&g_fd_status, v));
 }
 
@@ -2373,12 +2379,13 @@ cudaError_t read_status(unsigned* value, cudaStream_t stream, bool clear) {
     static std::mutex mutex;
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return e;
-    unsigned* word[3];
-    if ((e = status_word_tables(&word[0])) != cudaSuccess || (e = status_word_store(&word[1])) != cudaSuccess ||
-        (e = status_word_prompt(&word[2])) != cudaSuccess)
-        return e;
+    StatusWords s;
+    int n = 0;
+    for (const auto get : {status_word_tables, status_word_store, status_word_prompt, status_word_rope, status_word_pages,
+                           status_word_copy})
+        if ((e = get(&s.word[n++])) != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mutex);
-    fd_status_kernel<<<1, 1, 0, stream>>>(word[0], word[1], word[2], clear);
+    fd_status_kernel<<<1, 1, 0, stream>>>(s, clear);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = cudaMemcpyFromSymbolAsync(value, g_joined, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, stream);
     if (e != cudaSuccess) return e;

@@ -12,13 +12,10 @@
 // Bound by HBM for many rows (2 bytes in, 1 out per value) and by latency for
 // few: slots -> rows and old scale -> maximum -> stores.  10194 rows of 8 heads
 // (62.7 MB): 20 us, 3.1 TB/s; 64 single rows: 3.4 us.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include <initializer_list>
 #include <type_traits>
 
+#include "fd_convert.cuh"
 #include "fd_device.cuh"
 #include "fd_internal.h"
 
@@ -32,37 +29,12 @@ constexpr unsigned kFullMask = 0xffffffffu;
 constexpr int kStoreWarps = 8;
 constexpr int kKeep = 8;                // 16-byte pieces of the rows a lane keeps between the two passes
 
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
-    __half2 h;
-    memcpy(&h, &w, 4);
-    return __half22float2(h);
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
 // the smallest power of two s >= 2^-126 with amax <= 448 s
 __device__ __forceinline__ float scale_for(float amax) {
     const uint32_t u = __float_as_uint(amax);
     const int e = static_cast<int>(u >> 23) - 126;   // amax = f 2^e, f in [0.5, 1)
     const int k = (u & 0x7fffffu) <= 0x600000u ? e - 9 : e - 8;
     return __uint_as_float(static_cast<uint32_t>(max(k, -126) + 127) << 23);
-}
-
-// two values to E4M3, nearest even; NaN stays NaN, and with SPECIAL infinities
-// become NaN (the conversion would make them 448)
-template <bool SPECIAL>
-__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
-    if constexpr (SPECIAL) {
-        const float nan = __uint_as_float(0x7fc00000u);
-        a = fabsf(a) <= 3.402823466e38f ? a : nan;
-        b = fabsf(b) <= 3.402823466e38f ? b : nan;
-    }
-    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Quotient by s: exact through the reciprocal where s is a power of two (the

@@ -14,6 +14,7 @@
 // inputs are written behind a cluster barrier, after every CTA has read them.
 // 64 requests of one token: 3.1 us; 60000 tokens of 8 requests: 10.5 us.
 #include "../../include/fd.h"
+#include "fd_cluster.cuh"
 #include "fd_device.cuh"
 #include "fd_internal.h"
 
@@ -22,32 +23,6 @@ namespace fdk {
 namespace {
 
 __device__ unsigned int g_status = 0;   // this file's bits of the device status word
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
-
-// Inclusive prefix sum over the CTA of one value per thread; `total` gets the
-// sum.  warp_sums: 32 values of shared memory, free again after the call's
-// last barrier.
-__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    long long before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        const long long s = warp_sums[w];
-        if (w < warp) before += s;
-        all += s;
-    }
-    __syncthreads();
-    total = all;
-    return x + before;
-}
 
 __global__ void __launch_bounds__(1024) fd_page_tables_kernel(const PageParams p) {
     // per sequence: first new token of the step, first new page (-1: the

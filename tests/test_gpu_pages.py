@@ -1,0 +1,535 @@
+"""fd_page_fork, fd_page_trim, fd_page_compact and fd_page_copy on the GPU: whole
+numbers and bytes, so equal to the plain implementations of pages_ref.py."""
+import numpy as np
+import pytest
+import torch
+
+import pages_ref as ref
+import split_kv_gb300 as fd
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from split_kv_gb300 import _build
+    _build.build()
+    torch.cuda.set_device(DEV)
+    fd.fd_device_status(clear=True)
+    yield
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    yield
+    assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+class State:
+    """Lengths, tables, sharing counts and the free stack of a pool, as lists."""
+
+    def __init__(self, seed, batch, page, width, held=0.6, spare=40, longest=None, empty=0):
+        r = self.r = np.random.default_rng(seed)
+        self.page, self.width = page, width
+        longest = page * width if longest is None else longest
+        self.lens = [int(x) for x in r.integers(0, longest + 1, size=batch)]
+        for b in range(batch):
+            if r.random() < 0.2:
+                self.lens[b] = self.lens[b] // page * page
+            if r.random() >= held or b >= batch - empty:
+                self.lens[b] = 0
+        have = [-(-x // page) for x in self.lens]
+        self.n_pages = sum(have) + spare
+        perm = [int(x) for x in r.permutation(self.n_pages)]
+        self.table, at = [], 0
+        for h in have:
+            self.table.append(perm[at:at + h] + [-9] * (width - h))
+            at += h
+        self.free = perm[at:]
+        self.count = len(self.free)
+        self.free += [-5] * (self.n_pages - self.count + 3)
+        self.shares = [0] * self.n_pages
+
+    def take(self, out):
+        self.lens, self.count, self.table, self.free = out["lens"], out["count"], out["table"], out["free"]
+        self.shares = out["shares"] if out["shares"] is not None else self.shares
+
+    def forked(self, n):
+        """n forks of random parts into sequences that hold nothing."""
+        empty = [b for b, x in enumerate(self.lens) if x == 0]
+        full = [b for b, x in enumerate(self.lens) if x > 0]
+        n = min(n, len(empty))
+        if not full or n == 0:
+            return [], [], []
+        children = [int(x) for x in self.r.permutation(empty)[:n]]
+        parents = [int(self.r.choice(full)) for _ in range(n)]
+        keep = [int(self.r.integers(0, self.lens[p] + 1)) if self.r.random() < 0.6 else self.lens[p] for p in parents]
+        return parents, children, keep
+
+
+def device(s, alias, n_lists, shared=True):
+    t = dict(lens=i32(s.lens), count=i32([s.count]), table=i32(s.table).view(len(s.lens), s.width), free=i32(s.free),
+             shares=i32(s.shares) if shared else None, src=i32([77] * n_lists), dst=i32([78] * n_lists), n=i32([79]))
+    t["lens_out"], t["count_out"] = (t["lens"], t["count"]) if alias else (torch.full_like(t["lens"], 99), torch.full_like(t["count"], 99))
+    t["desc"] = fd.make_page_desc(t["table"], t["free"], None, copies=t["src"], page_size=s.page, n_pages=s.n_pages)
+    return t
+
+
+def run_fork(s, parents, children, keep, alias=False, stream=None):
+    t = device(s, alias, max(1, len(parents)))
+    args = (t["desc"], i32(parents), i32(children), None if keep is None else i32(keep), t["lens"], t["free"], t["count"], t["table"],
+            t["shares"], t["lens_out"], t["count_out"], t["src"], t["dst"], t["n"])
+    fd.check(fd.fd_page_fork(*args), "fd_page_fork")
+    torch.cuda.synchronize()
+    return t
+
+
+def run_trim(s, keep, alias=False, shared=True):
+    t = device(s, alias, len(s.lens) if shared else 0, shared)
+    lists = (t["src"], t["dst"], t["n"]) if shared else (None, None, t["n"])
+    fd.check(fd.fd_page_trim(t["desc"], i32(keep), t["lens"], t["free"], t["count"], t["table"], t["shares"], t["lens_out"],
+                             t["count_out"], *lists), "fd_page_trim")
+    torch.cuda.synchronize()
+    return t
+
+
+def run_compact(s, n_keep, n_lists, alias=False, shared=True):
+    t = device(s, alias, n_lists, shared)
+    fd.check(fd.fd_page_compact(t["desc"], n_keep, t["lens"], t["free"], t["count"], t["table"], t["shares"], t["count_out"], t["src"],
+                                t["dst"], t["n"]), "fd_page_compact")
+    torch.cuda.synchronize()
+    t["lens_out"] = t["lens"]
+    return t
+
+
+def same(t, want, bad=False):
+    for name, a in (("count", t["count_out"]), ("n", t["n"])):
+        assert int(a) == want[name], name
+    for name in ("table", "free", "shares", "src", "dst"):
+        if want.get(name) is not None and t[name] is not None:
+            assert t[name].tolist() == want[name], name
+    if "lens" in want:
+        assert t["lens_out"].tolist() == want["lens"]
+    assert fd.fd_device_status(clear=True) == (fd.FD_ERR_DEVICE_BOUNDS if bad else fd.FD_OK)
+
+
+def want_fork(s, parents, children, keep):
+    n = max(1, len(parents))
+    return ref.fork(parents, children, keep, s.lens, s.free, s.count, s.table, s.shares, s.page, s.n_pages, [77] * n, [78] * n)
+
+
+def want_trim(s, keep, shared=True):
+    n = len(s.lens) if shared else 0
+    return ref.trim(keep, s.lens, s.free, s.count, s.table, s.shares if shared else None, s.page, s.n_pages, [77] * n, [78] * n)
+
+
+def want_compact(s, n_keep, n, shared=True):
+    return ref.compact(n_keep, s.lens, s.free, s.count, s.table, s.shares if shared else None, s.page, s.n_pages, [77] * n, [78] * n)
+
+
+SIZES = [(2, 16, 5, 1), (9, 8, 40, 4), (40, 16, 130, 25), (300, 32, 12, 200), (64, 16, 1100, 60), (3000, 16, 3, 1500), (8192, 8, 2, 5000)]
+
+
+# ------------------------------------------------------------------ forks
+@pytest.mark.parametrize("batch,page,width,n", SIZES)
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("whole", [False, True])
+def test_fork(batch, page, width, n, alias, whole):
+    s = State(batch + page, batch, page, width, held=0.45, spare=n + 20, empty=1)
+    parents, children, keep = s.forked(n)
+    keep = None if whole else keep
+    want, bad = want_fork(s, parents, children, keep)
+    assert not bad
+    same(run_fork(s, parents, children, keep, alias), want)
+
+
+def test_fork_many_of_one_parent():
+    for tokens in (16 * 700, 16 * 700 + 5):
+        s = State(3, 200, 16, 701, held=0.0, spare=900)
+        s.table[4] = s.free[:701]
+        s.free = s.free[701:900] + [-5] * 30
+        s.lens[4], s.count = tokens, 199
+        children = [b for b in range(200) if b != 4]
+        keep = [tokens if b % 5 else tokens - 16 * (b % 3) for b in children]
+        for k in (None, keep):
+            want, bad = want_fork(s, [4] * 199, children, k)
+            assert not bad
+            same(run_fork(s, [4] * 199, children, k), want)
+
+
+@pytest.mark.parametrize("what", ["few pages", "no pages", "child twice", "child holds tokens", "itself", "too long", "negative", "outside",
+                                  "bad length", "free count", "bad free page", "bad table entry", "child of a child"])
+def test_fork_reports_what_does_not_fit(what):
+    s = State(5, 12, 16, 30, held=1.0, spare=30, empty=6)
+    parents, children, keep = [0, 1, 2, 3, 1], [6, 7, 8, 9, 10], [20, 35, 17, 33, 40]
+    s.lens[:4], s.n_pages = [200, 100, 90, 50], 100
+    perm = [int(x) for x in s.r.permutation(100)]
+    s.table = [perm[7 * b:7 * b + 7] * 2 + [-9] * 16 for b in range(12)]
+    s.free, s.count, s.shares = perm[84:] + [-5] * 9, 16, [0] * 100
+    s.lens[4:] = [0] * 8
+    s.lens[11] = 3
+    if what == "few pages":
+        s.count = 3
+    elif what == "no pages":
+        s.count = 0
+    elif what == "child twice":
+        children[3] = 7
+    elif what == "child holds tokens":
+        children[2] = 11
+    elif what == "itself":
+        children[2] = 2
+    elif what == "too long":
+        keep[1] = 101
+    elif what == "negative":
+        keep[1] = -1
+    elif what == "outside":
+        parents[0], children[1], parents[2], children[3] = 12, -1, -1, 12
+    elif what == "bad length":
+        s.lens[1] = 16 * 30 + 1
+    elif what == "free count":
+        s.count = len(s.free) + 4
+    elif what == "bad free page":
+        s.free[14] = 100
+    elif what == "bad table entry":
+        s.table[0][0] = 100
+        s.table[1][1] = -1
+    elif what == "child of a child":          # (nothing to report: parents as they were, without tokens)
+        parents[3], keep[3] = 6, 0
+    want, bad = want_fork(s, parents, children, keep)
+    assert bad == (what != "child of a child")
+    same(run_fork(s, parents, children, keep), want, bad)
+
+
+def test_fork_of_nothing():
+    s = State(6, 5, 16, 4)
+    want, bad = want_fork(s, [], [], [])
+    t = device(s, False, 1)
+    fd.check(fd.fd_page_fork(t["desc"], None, None, None, t["lens"], t["free"], t["count"], t["table"], t["shares"], t["lens_out"],
+                             t["count_out"], t["src"], t["dst"], t["n"], n_forks=0))
+    same(t, want, bad)
+
+
+# ------------------------------------------------------------------ trims
+def shared_state(seed, batch, page, width, n):
+    """A state after forks and some trims, so that pages are shared in all ways."""
+    s = State(seed, batch, page, width, held=0.5, spare=2 * n + batch + 20)
+    for _ in range(2):
+        parents, children, keep = s.forked(n)
+        out, bad = want_fork(s, parents, children, keep)
+        assert not bad
+        s.take(out)
+    return s
+
+
+def random_keep(s, r):
+    keep = []
+    for x in s.lens:
+        u = r.random()
+        keep.append(0 if u < 0.2 else x if u < 0.3 else -1 if u < 0.35 else int(r.integers(0, x + 1)) if u < 0.7 else max(0, x - int(r.integers(0, 6))) if u < 0.9
+                    else x // s.page * s.page // 2)
+    return keep
+
+
+@pytest.mark.parametrize("batch,page,width,n", SIZES)
+@pytest.mark.parametrize("alias", [False, True])
+def test_trim(batch, page, width, n, alias):
+    s = shared_state(batch + 7 * page, batch, page, width, n)
+    for _ in range(3):
+        keep = random_keep(s, s.r)
+        want, bad = want_trim(s, keep)
+        assert not bad
+        same(run_trim(s, keep, alias), want)
+        s.take(want)
+    want, bad = want_trim(s, [0] * batch)              # and everything goes back
+    same(run_trim(s, [0] * batch, alias), want)
+    assert want["count"] == s.n_pages and not any(want["shares"]) and sorted(want["free"][:s.n_pages]) == list(range(s.n_pages))
+
+
+@pytest.mark.parametrize("batch,page,width,n", SIZES)
+def test_trim_without_shares(batch, page, width, n):
+    s = State(batch * 3 + page, batch, page, width)
+    keep = random_keep(s, s.r)
+    want, bad = want_trim(s, keep, False)
+    assert not bad
+    same(run_trim(s, keep, shared=False), want)
+
+
+def test_trim_undoes_a_step():
+    s = State(31, 50, 16, 40, held=1.0, spare=900, longest=300)
+    new = [int(x) for x in s.r.integers(0, 200, size=50)]
+    t = device(s, False, 50)
+    slots = torch.zeros(sum(new), dtype=torch.int64, device=DEV)
+    d = fd.make_page_desc(t["table"], t["free"], slots, page_size=16, n_pages=s.n_pages)
+    fd.check(fd.fd_page_tables(d, t["lens"], i32(new), t["free"], t["count"], t["table"], t["lens_out"], t["count_out"], None, slots, None))
+    fd.check(fd.fd_page_trim(t["desc"], t["lens"], t["lens_out"], t["free"], t["count_out"], t["table"], t["shares"], t["lens_out"],
+                             t["count_out"], t["src"], t["dst"], t["n"]))
+    assert t["lens_out"].tolist() == s.lens and int(t["count_out"]) == s.count and t["free"].tolist() == s.free
+
+
+@pytest.mark.parametrize("what", ["few pages", "no pages", "bad length", "negative length", "bad page", "bad tail", "let go twice", "no room",
+                                  "free count", "bad free page"])
+def test_trim_reports_what_does_not_fit(what):
+    s = State(9, 8, 16, 20, held=1.0, spare=30, empty=4)
+    s.lens = [200, 100, 90, 50, 0, 0, 0, 0]
+    s.n_pages, s.shares = 80, [0] * 80
+    perm = [int(x) for x in s.r.permutation(80)]
+    s.table = [perm[13 * b:13 * b + 13] + [-9] * 7 for b in range(4)] + [[-9] * 20 for _ in range(4)]
+    s.free, s.count = perm[52:] + [-5] * 52, 28
+    out, bad = want_fork(s, [0, 0, 1, 1], [4, 5, 6, 7], [190, 200, 100, 33])
+    assert not bad
+    s.take(out)
+    keep = [70, 50, 10, 0, 71, 64, 40, 20]
+    if what == "few pages":
+        s.count = 2
+    elif what == "no pages":
+        s.count = 0
+    elif what == "bad length":
+        s.lens[1] = 16 * 20 + 1
+    elif what == "negative length":
+        s.lens[2] = -4
+    elif what == "bad page":
+        s.table[3][1] = 80
+        s.table[0][9] = -1
+    elif what == "bad tail":
+        s.table[0][4] = 80
+    elif what == "let go twice":
+        s.table[3][0] = s.table[2][5]
+        s.shares[s.table[2][5]] = 0
+    elif what == "no room":
+        s.free = s.free[:s.count + 3]
+    elif what == "free count":
+        s.count = -1
+    elif what == "bad free page":
+        s.free[s.count - 1] = 80
+    want, bad = want_trim(s, keep)
+    assert bad
+    same(run_trim(s, keep), want, True)
+
+
+def test_trim_of_no_sequences():
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    table, free = torch.empty(0, 4, dtype=torch.int32, device=DEV), i32([3, 2, 1])
+    d = fd.make_page_desc(table, free, None, page_size=16, n_pages=4)
+    out = i32([-1])
+    fd.check(fd.fd_page_trim(d, e, e, free, i32([2]), table, None, e, out))
+    assert int(out) == 2 and free.tolist() == [3, 2, 1]
+
+
+# ------------------------------------------------------------------ compaction
+@pytest.mark.parametrize("batch,page,width,n", SIZES)
+@pytest.mark.parametrize("part", [0.0, 0.3, 0.8, 1.0])
+def test_compact(batch, page, width, n, part):
+    s = shared_state(batch + 11 * page, batch, page, width, n)
+    keep = random_keep(s, s.r)
+    s.take(want_trim(s, keep)[0])
+    n_keep = int(s.n_pages * part)
+    want, bad = want_compact(s, n_keep, s.n_pages)
+    same(run_compact(s, n_keep, s.n_pages, alias=batch % 2 == 0), want, bad)
+    few = max(0, want["n"] - 2)
+    want, bad = want_compact(s, n_keep, few)                  # a copy list that is too short
+    same(run_compact(s, n_keep, few), want, bad)
+    want, bad = want_compact(s, n_keep, s.n_pages, False)
+    same(run_compact(s, n_keep, s.n_pages, shared=False), want, bad)
+
+
+def test_compact_a_large_pool():
+    """More free pages than one round of the filter holds, and more than one word of the map a thread."""
+    s = State(17, 40, 8, 300, held=0.9, spare=400000)
+    for n_keep in (1000, 200000, 399000):
+        want, bad = want_compact(s, n_keep, s.n_pages)
+        assert bad == (n_keep == 1000)
+        same(run_compact(s, n_keep, s.n_pages), want, bad)
+
+
+@pytest.mark.parametrize("what", ["bad length", "bad page", "bad free page", "free count"])
+def test_compact_reports(what):
+    s = State(19, 6, 16, 20, held=1.0, spare=50)
+    s.lens[2], s.lens[3] = max(s.lens[2], 40), max(s.lens[3], 40)
+    if what == "bad length":
+        s.lens[2] = 16 * 20 + 1
+    elif what == "bad page":
+        s.table[3][1], s.table[3][0] = s.n_pages, -1
+    elif what == "bad free page":
+        s.free[3], s.free[4] = -1, s.n_pages
+    else:
+        s.count = len(s.free) + 1
+    want, bad = want_compact(s, s.n_pages // 2, s.n_pages)
+    assert bad
+    same(run_compact(s, s.n_pages // 2, s.n_pages), want, True)
+
+
+# ------------------------------------------------------------------ copies
+def copied(x, pairs):
+    y = x.clone()
+    for a, b in pairs:
+        if a >= 0 and b >= 0:
+            y[b] = x[a]
+    return y
+
+
+def rand_bytes(seed, dtype, *shape):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    return torch.randint(0, 256, (n,), dtype=torch.uint8, device=DEV, generator=g).view(dtype).view(shape)
+
+
+def bits(x):
+    return x.contiguous().view(torch.uint8)
+
+
+POOLS = {
+    "bf16": lambda P: [rand_bytes(k, torch.bfloat16, P, 8, 16, 128) for k in range(5)],
+    "many": lambda P: [rand_bytes(k, torch.float16, P, 2, 8, 128) for k in range(70)],
+    "tokens first": lambda P: [rand_bytes(1, torch.float16, P, 16, 4, 128).permute(0, 2, 1, 3)],
+    "heads apart": lambda P: [rand_bytes(2, torch.float16, 3, P, 16, 128).permute(1, 0, 2, 3)],
+    "part of rows": lambda P: [rand_bytes(3, torch.bfloat16, P, 2, 16, 2, 128)[:, :, :, k] for k in range(2)],
+    "e4m3 and scales": lambda P: [rand_bytes(4, torch.float8_e4m3fn, P, 8, 64, 128)] + [rand_bytes(5 + k, torch.float32, P, 8, 2) for k in range(3)],
+    "odd": lambda P: [rand_bytes(6, torch.uint8, P, 5, 7), rand_bytes(7, torch.int16, P, 3, 5), rand_bytes(8, torch.float32, P, 7),
+                      rand_bytes(9, torch.float64, P, 3), rand_bytes(10, torch.uint8, P)],
+    "offset": lambda P: [rand_bytes(11, torch.float32, P * 40 + 1)[1:].view(P, 2, 20), rand_bytes(12, torch.bfloat16, P * 64 + 3)[3:].view(P, 64)],
+    "large": lambda P: [rand_bytes(13, torch.float16, P, 16, 128, 128)],
+    "steps": lambda P: [rand_bytes(14, torch.float32, P, 6)[:, ::2]],
+}
+
+
+@pytest.mark.parametrize("name", sorted(POOLS))
+@pytest.mark.parametrize("pairs", [1, 7, 11])
+def test_copy(name, pairs):
+    P = 23
+    pools = POOLS[name](P)
+    perm = [int(x) for x in np.random.default_rng(pairs).permutation(P)]
+    src, dst = perm[:pairs], perm[pairs:2 * pairs]
+    if pairs > 1:
+        src[1] = src[0]                       # one page into two
+        src[2], dst[3] = -1, -1               # left out
+        dst[4] = src[4]
+    want = [copied(x, zip(src, dst)) for x in pools]
+    fd.check(fd.fd_page_copy(fd.make_pools(pools), i32(src), i32(dst)))
+    for x, y in zip(pools, want):
+        assert torch.equal(bits(x), bits(y))
+
+
+@pytest.mark.parametrize("count", [0, 3, 9, 20, -2])
+def test_copy_counts(count):
+    P = 40
+    x = rand_bytes(1, torch.float16, P, 4, 16, 128)
+    src, dst = list(range(9)), list(range(20, 29))
+    want = copied(x, list(zip(src, dst))[:max(0, count)])
+    fd.check(fd.fd_page_copy(fd.make_pools([x]), i32(src), i32(dst), i32([count])))
+    assert torch.equal(bits(x), bits(want))
+
+
+def test_copy_reports_pages_outside_the_pool():
+    x = rand_bytes(2, torch.float16, 10, 4, 16, 128)
+    want = copied(x, [(1, 2)])
+    fd.check(fd.fd_page_copy(fd.make_pools([x]), i32([10, 1, 3]), i32([4, 2, 1 << 30])))
+    assert torch.equal(bits(x), bits(want))
+    assert fd.fd_device_status(clear=True) == fd.FD_ERR_DEVICE_BOUNDS
+
+
+def test_copy_writes_nothing_else():
+    """The bytes between the rows of strided pools, and behind the last page, stay."""
+    back = rand_bytes(3, torch.float16, 9, 4, 20, 160)
+    x = back[:, :, :16, :128]
+    before = back.clone()
+    fd.check(fd.fd_page_copy(fd.make_pools([x]), i32([1, 2]), i32([8, 0])))
+    want = before.clone()
+    want[8, :, :16, :128], want[0, :, :16, :128] = before[1, :, :16, :128], before[2, :, :16, :128]
+    assert torch.equal(bits(back), bits(want))
+
+
+# ------------------------------------------------------------------ streams and graphs
+def test_page_operators_captured():
+    """Fork, copy, trim and compaction in one graph, replayed over other lengths in the same buffers."""
+    s = State(41, 20, 16, 30, held=1.0, spare=200, empty=8)
+    cache = rand_bytes(5, torch.float16, s.n_pages, 2, 16, 128)
+    start = cache.clone()
+    t = device(s, False, s.n_pages)
+    fork = device(s, False, 8)
+    lens2, count2, count3 = (torch.zeros_like(x) for x in (t["lens"], t["count"], t["count"]))
+    parents, children, keep = i32([0] * 8), i32(list(range(12, 20))), i32([0] * 8)
+    cut = i32([-1] * 20)
+    pools = fd.make_pools([cache])
+
+    def step():
+        fd.check(fd.fd_page_fork(fork["desc"], parents, children, keep, t["lens"], t["free"], t["count"], t["table"], t["shares"],
+                                 t["lens_out"], t["count_out"], fork["src"], fork["dst"], fork["n"]))
+        fd.check(fd.fd_page_copy(pools, fork["src"], fork["dst"], fork["n"]))
+        fd.check(fd.fd_page_trim(t["desc"], cut, t["lens_out"], t["free"], t["count_out"], t["table"], t["shares"], lens2, count2,
+                                 t["src"], t["dst"], t["n"]))
+        fd.check(fd.fd_page_copy(pools, t["src"], t["dst"], t["n"]))
+        fd.check(fd.fd_page_compact(t["desc"], s.n_pages * 3 // 4, lens2, t["free"], count2, t["table"], t["shares"], count3, t["src"],
+                                    t["dst"], t["n"]))
+        fd.check(fd.fd_page_copy(pools, t["src"], t["dst"], t["n"]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                      # (attributes are set once per context, ahead of the capture)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    fd.fd_device_status(clear=True)
+    for seed in range(3):
+        n = State(50 + seed, 20, 16, 30, held=1.0, spare=200, empty=8)
+        n.n_pages = s.n_pages
+        perm = [int(x) for x in n.r.permutation(s.n_pages)]
+        n.lens = [min(x, 300) for x in n.lens]
+        have = [-(-x // 16) for x in n.lens]
+        while sum(have) + 60 > s.n_pages * 3 // 4:
+            n.lens = [x // 2 for x in n.lens]
+            have = [-(-x // 16) for x in n.lens]
+        at = np.concatenate([[0], np.cumsum(have)])
+        n.table = [perm[at[b]:at[b + 1]] + [-9] * (30 - have[b]) for b in range(20)]
+        n.free = perm[at[-1]:]
+        n.count = len(n.free)
+        n.free += [-5] * (len(s.free) - n.count)
+        n.shares = [0] * s.n_pages
+        par, chi, kp = n.forked(8)
+        kt = [int(n.r.integers(-1, x + 1)) for x in n.lens[:12]] + [int(n.r.integers(0, k + 1)) for _, k in sorted(zip(chi, kp))]
+        for dst, v in ((t["lens"], n.lens), (t["count"], [n.count]), (t["table"], n.table), (t["free"], n.free), (t["shares"], n.shares),
+                       (parents, par), (children, chi), (keep, kp), (cut, kt)):
+            dst.copy_(i32(v).view(dst.shape))
+        cache.copy_(start)
+        want = start.clone()
+        # the tokens that each sequence stands for, followed through the reference
+        out, bad = want_fork(n, par, chi, kp)
+        assert not bad
+        want = copied(want, zip(out["src"][:out["n"]], out["dst"][:out["n"]]))
+        n.take(out)
+        out, bad = ref.trim(kt, n.lens, n.free, n.count, n.table, n.shares, 16, n.n_pages, [77] * n.n_pages, [78] * n.n_pages)
+        assert not bad
+        want = copied(want, zip(out["src"][:out["n"]], out["dst"][:out["n"]]))
+        n.take(out)
+        out, bad = want_compact(n, n.n_pages * 3 // 4, n.n_pages)
+        assert not bad
+        want = copied(want, zip(out["src"][:out["n"]], out["dst"][:out["n"]]))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert t["table"].tolist() == out["table"] and t["shares"].tolist() == out["shares"] and int(count3) == out["count"]
+        assert lens2.tolist() == n.lens and t["free"].tolist() == out["free"] and int(t["n"]) == out["n"]
+        assert torch.equal(bits(cache), bits(want))
+
+
+def test_two_streams_at_once():
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    s = [shared_state(70 + k, 300, 16, 40, 100) for k in range(2)]
+    keep = [random_keep(x, x.r) for x in s]
+    want = [want_trim(x, k)[0] for x, k in zip(s, keep)]
+    t = [device(x, False, 300) for x in s]
+    cut = [i32(k) for k in keep]
+    torch.cuda.synchronize()
+    for x, k, st in zip(t, cut, (a, b)):
+        fd.check(fd.fd_page_trim(x["desc"], k, x["lens"], x["free"], x["count"], x["table"], x["shares"], x["lens_out"], x["count_out"],
+                                 x["src"], x["dst"], x["n"], stream=st))
+    torch.cuda.synchronize()
+    for x, w in zip(t, want):
+        same(x, w)
