@@ -829,38 +829,19 @@ fd_status fd_qkv_rope(const fd_rope_desc* d, const void* q, const void* k, const
     if (q != nullptr && q == q_out && (d->q_stride_t != d->q_out_stride_t || d->q_stride_h != d->q_out_stride_h)) return FD_ERR_INVALID_ARG;
     if (k != nullptr && k == k_out && (d->k_src_stride_t != d->k_out_stride_t || d->k_src_stride_h != d->k_out_stride_h))
         return FD_ERR_INVALID_ARG;
+    const bool fp8 = cached && d->cache_dtype == FD_E4M3;
+    const bool norm_q = (d->norm & FD_NORM_Q) != 0, norm_k = (d->norm & FD_NORM_K) != 0;
     fdk::RopeParams p = {};
-    p.q = q;
-    p.k = k;
-    p.v = v;
-    p.q_out = q_out;
-    p.k_out = k_out;
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
-    p.q_w = q_weight;
-    p.k_w = k_weight;
+    p.side[0] = {q, q_out, nullptr, norm_q ? q_weight : nullptr, d->q_stride_t, d->q_stride_h, d->q_out_stride_t,
+                 d->q_out_stride_h, 0, 0, 0, norm_q && q_weight != nullptr ? d->q_w_stride_h : 0, d->n_q_heads, norm_q, 1.f};
+    p.side[1] = {k, k_out, k_cache, norm_k ? k_weight : nullptr, d->k_src_stride_t, d->k_src_stride_h, d->k_out_stride_t,
+                 d->k_out_stride_h, d->k_stride_b, d->k_stride_h, d->k_stride_t,
+                 norm_k && k_weight != nullptr ? d->k_w_stride_h : 0, d->n_kv_heads, norm_k, fp8 ? 1.f / d->k_scale : 1.f};
+    p.side[2] = {v, nullptr, v_cache, nullptr, d->v_src_stride_t, d->v_src_stride_h, 0, 0, d->v_stride_b, d->v_stride_h,
+                 d->v_stride_t, 0, d->n_kv_heads, 0, fp8 ? 1.f / d->v_scale : 1.f};
     p.inv_freq = inv_freq;
     p.positions = positions;
     p.slots = slots;
-    p.q_t = d->q_stride_t;
-    p.q_h = d->q_stride_h;
-    p.k_t = d->k_src_stride_t;
-    p.k_h = d->k_src_stride_h;
-    p.v_t = d->v_src_stride_t;
-    p.v_h = d->v_src_stride_h;
-    p.qo_t = d->q_out_stride_t;
-    p.qo_h = d->q_out_stride_h;
-    p.ko_t = d->k_out_stride_t;
-    p.ko_h = d->k_out_stride_h;
-    p.kc_b = d->k_stride_b;
-    p.kc_h = d->k_stride_h;
-    p.kc_t = d->k_stride_t;
-    p.vc_b = d->v_stride_b;
-    p.vc_h = d->v_stride_h;
-    p.vc_t = d->v_stride_t;
-    p.qw_h = d->q_w_stride_h;
-    p.kw_h = d->k_w_stride_h;
-    const bool fp8 = cached && d->cache_dtype == FD_E4M3;
     if (cached) {
         const bool paged = d->page_size > 0;
         p.row_tokens = paged ? d->page_size : static_cast<int32_t>(d->kv_extent);
@@ -868,15 +849,10 @@ fd_status fd_qkv_rope(const fd_rope_desc* d, const void* q, const void* k, const
         p.row_shift = paged ? log2_of(d->page_size) : -1;
     }
     p.n_tokens = d->n_tokens;
-    p.n_q_heads = d->n_q_heads;
-    p.n_kv_heads = d->n_kv_heads;
     p.rot_dim = d->rot_dim;
-    p.norm = d->norm;
     p.w_dtype = d->w_dtype == FD_F16 ? 0 : d->w_dtype == FD_BF16 ? 1 : 2;
     p.eps = d->eps;
     p.rot_scale = d->rot_scale;
-    p.k_inv = fp8 ? 1.f / d->k_scale : 1.f;
-    p.v_inv = fp8 ? 1.f / d->v_scale : 1.f;
     return fdk::launch_rope(p, d->dtype == FD_BF16, d->interleaved != 0, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? FD_OK
                : FD_ERR_CUDA;

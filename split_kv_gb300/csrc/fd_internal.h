@@ -210,27 +210,25 @@ cudaError_t launch_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const 
 
 // ---- norms and rotation into a cache; forks, trims, compaction and copies of pages
 
+struct RopeSide {                   // queries, keys or values; strides in elements
+    const void* src;
+    void* out;                      // or null
+    void* cache;                    // or null
+    const void* weights;            // or null
+    int64_t src_t, src_h, out_t, out_h, cache_b, cache_h, cache_t, w_h;
+    int32_t heads, norm;
+    float inv;                      // 1 / scale of an E4M3 cache
+};
 struct RopeParams {
-    const void* q;
-    const void* k;
-    const void* v;
-    void* q_out;
-    void* k_out;                    // or null
-    void* k_cache;                  // or null, and v_cache with it
-    void* v_cache;
-    const void* q_w;                // or null
-    const void* k_w;
+    RopeSide side[3];
     const float* inv_freq;
     const int32_t* positions;
     const int64_t* slots;
-    int64_t q_t, q_h, k_t, k_h, v_t, v_h, qo_t, qo_h, ko_t, ko_h;   // elements
-    int64_t kc_b, kc_h, kc_t, vc_b, vc_h, vc_t, qw_h, kw_h;
     int64_t n_slots;                // places in the caches
     int32_t row_tokens;             // tokens per page, or per sequence of a contiguous cache
     int32_t row_shift;              // log2(row_tokens) of pages; -1 for a contiguous cache
-    int32_t n_tokens, n_q_heads, n_kv_heads;
-    int32_t rot_dim, norm, w_dtype; // FD_NORM_* bits; 0 f16, 1 bf16, 2 f32
-    float eps, rot_scale, k_inv, v_inv;
+    int32_t n_tokens, rot_dim, w_dtype;   // w_dtype: 0 f16, 1 bf16, 2 f32
+    float eps, rot_scale;
 };
 cudaError_t launch_rope(const RopeParams& p, bool bf16, bool interleaved, bool fp8_cache, cudaStream_t stream);
 
