@@ -493,7 +493,7 @@ fd_status fd_prompt(const fd_prompt_desc* desc, const void* q, const void* k, co
  * of this file hold.
  *
  * Pages that several sequences hold: shares[p] (device int32[n_pages]) is the
- * number of sequences that hold page p beyond the first, so 0 for a page of one
+ * number of sequences that hold page p beyond the first (below 2^15), so 0 for a page of one
  * sequence and for a free one, and fd_page_tables needs to know nothing of it.
  * A page is shared only while it is full for every sequence that holds it: a
  * fork copies a page of which it takes a part, and a trim that ends inside a
@@ -629,7 +629,7 @@ fd_status fd_page_trim(const fd_page_desc* desc, const int32_t* keep, const int3
                        int32_t* shares, int32_t* seqlens_out, int32_t* free_count_out,
                        int32_t* copy_src, int32_t* copy_dst, int32_t* copy_count, void* stream);
 
-#define FD_MAX_COMPACT_PAGES (1 << 22)   /* pages of the pool behind n_keep in one fd_page_compact call */
+#define FD_MAX_COMPACT_PAGES (1 << 19)   /* pages of the pool behind n_keep in one fd_page_compact call */
 
 /* Compaction: the pages from n_keep on that the tables hold move to free pages
  * below n_keep, so that the high end of the pool can be given up.  F: the entries

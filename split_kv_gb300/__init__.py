@@ -41,7 +41,7 @@ FD_FLAG_CUDA_CORES = 1
 FD_FLAG_TEST_DROP_FIRST_STAGE = 1 << 16
 FD_NORM_Q, FD_NORM_K = 1, 2
 FD_MAX_TABLE_BATCH = 8192
-FD_MAX_COMPACT_PAGES = 1 << 22
+FD_MAX_COMPACT_PAGES = 1 << 19
 
 LIB_PATH = _build.LIB_PATH
 
@@ -274,13 +274,24 @@ def _check_scales(desc, scales: FdKvScales) -> None:
         raise ValueError(f"scales {scales.shape} of {scales.block}-token blocks do not cover the cache")
 
 
-def _ints(name: str, t, n: int) -> None:
-    """t, if it is a tensor, holds n contiguous int32 (addresses and None go unchecked)."""
+_int32 = None
+
+
+def _i32(t, n: int, name: str):
+    """Address of n contiguous int32, checked if t is a tensor (addresses and None go unchecked)."""
+    global _int32
+    if t is None:
+        return None
     try:
-        if t.element_size() != 4 or t.is_floating_point() or t.nbytes < 4 * n or not t.is_contiguous():
+        dtype = t.dtype
+        if _int32 is None:
+            import torch
+            _int32 = torch.int32
+        if dtype is not _int32 or t.nbytes < 4 * n or not t.is_contiguous():
             raise ValueError(f"{name} must be {n} contiguous int32")
+        return t.data_ptr()
     except AttributeError:
-        pass
+        return _ptr(t)
 
 
 def check(status: int, what: str = "") -> int:
@@ -426,7 +437,7 @@ def fd_qkv_rope(desc: FdRopeDesc, q, k, v, q_weight, k_weight, inv_freq, positio
                 v_cache, stream=None) -> int:
     """Norms and rotation of a step's queries and keys, and the way of its keys and values into a cache."""
     n = desc.n_tokens
-    _ints("positions", positions, n)
+    pos = _i32(positions, n, "positions")
     try:
         if inv_freq is not None and (inv_freq.nbytes < 2 * desc.rot_dim or inv_freq.element_size() != 4 or not inv_freq.is_contiguous()):
             raise ValueError(f"inv_freq must be {desc.rot_dim // 2} contiguous float32")
@@ -438,58 +449,49 @@ def fd_qkv_rope(desc: FdRopeDesc, q, k, v, q_weight, k_weight, inv_freq, positio
     except AttributeError:
         pass
     return _load().fd_qkv_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-                               _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache),
-                               _stream(stream))
-
-
-def _check_page_lists(desc, seqlens, free_pages, block_table, shares, seqlens_out, copy_src, copy_dst) -> None:
-    _ints("seqlens", seqlens, desc.batch)
-    _ints("free_pages", free_pages, desc.n_free_max)
-    _ints("block_table", block_table, desc.batch * desc.max_pages_per_seq)
-    _ints("shares", shares, desc.n_pages)
-    _ints("seqlens_out", seqlens_out, desc.batch)
-    _ints("copy_src", copy_src, desc.n_slots)
-    _ints("copy_dst", copy_dst, desc.n_slots)
+                               pos, _ptr(slots), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _stream(stream))
 
 
 def fd_page_fork(desc: FdPageDesc, parents, children, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out,
                  free_count_out, copy_src, copy_dst, copy_count, n_forks: int | None = None, stream=None) -> int:
     """Sequences children[i] that share the pages of parents[i]'s first keep[i] tokens (None: of all)."""
     n = parents.numel() if n_forks is None else int(n_forks)
-    for name, t in (("parents", parents), ("children", children), ("keep", keep)):
-        _ints(name, t, n)
-    _check_page_lists(desc, seqlens, free_pages, block_table, shares, seqlens_out, copy_src, copy_dst)
-    return _load().fd_page_fork(ctypes.byref(desc), n, _ptr(parents), _ptr(children), _ptr(keep), _ptr(seqlens),
-                                _ptr(free_pages), _ptr(free_count), _ptr(block_table), _ptr(shares), _ptr(seqlens_out),
-                                _ptr(free_count_out), _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _stream(stream))
+    b, lists = desc.batch, desc.n_slots
+    return _load().fd_page_fork(ctypes.byref(desc), n, _i32(parents, n, "parents"), _i32(children, n, "children"),
+                                _i32(keep, n, "keep"), _i32(seqlens, b, "seqlens"), _i32(free_pages, desc.n_free_max, "free_pages"),
+                                _ptr(free_count), _i32(block_table, b * desc.max_pages_per_seq, "block_table"),
+                                _i32(shares, desc.n_pages, "shares"), _i32(seqlens_out, b, "seqlens_out"), _ptr(free_count_out),
+                                _i32(copy_src, lists, "copy_src"), _i32(copy_dst, lists, "copy_dst"), _ptr(copy_count),
+                                _stream(stream))
 
 
 def fd_page_trim(desc: FdPageDesc, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out, free_count_out,
                  copy_src=None, copy_dst=None, copy_count=None, stream=None) -> int:
     """Sequences cut to their first keep[b] tokens; pages that nobody holds any more go back to the free stack."""
-    _ints("keep", keep, desc.batch)
-    _check_page_lists(desc, seqlens, free_pages, block_table, shares, seqlens_out, copy_src, copy_dst)
-    return _load().fd_page_trim(ctypes.byref(desc), _ptr(keep), _ptr(seqlens), _ptr(free_pages), _ptr(free_count),
-                                _ptr(block_table), _ptr(shares), _ptr(seqlens_out), _ptr(free_count_out), _ptr(copy_src),
-                                _ptr(copy_dst), _ptr(copy_count), _stream(stream))
+    b, lists = desc.batch, desc.n_slots
+    return _load().fd_page_trim(ctypes.byref(desc), _i32(keep, b, "keep"), _i32(seqlens, b, "seqlens"),
+                                _i32(free_pages, desc.n_free_max, "free_pages"), _ptr(free_count),
+                                _i32(block_table, b * desc.max_pages_per_seq, "block_table"), _i32(shares, desc.n_pages, "shares"),
+                                _i32(seqlens_out, b, "seqlens_out"), _ptr(free_count_out), _i32(copy_src, lists, "copy_src"),
+                                _i32(copy_dst, lists, "copy_dst"), _ptr(copy_count), _stream(stream))
 
 
 def fd_page_compact(desc: FdPageDesc, n_keep: int, seqlens, free_pages, free_count, block_table, shares, free_count_out,
                     copy_src, copy_dst, copy_count, stream=None) -> int:
     """Held pages from n_keep on renamed to free pages below it, for the high end of a pool to be given up."""
-    _check_page_lists(desc, seqlens, free_pages, block_table, shares, None, copy_src, copy_dst)
-    return _load().fd_page_compact(ctypes.byref(desc), int(n_keep), _ptr(seqlens), _ptr(free_pages), _ptr(free_count),
-                                   _ptr(block_table), _ptr(shares), _ptr(free_count_out), _ptr(copy_src), _ptr(copy_dst),
+    b, lists = desc.batch, desc.n_slots
+    return _load().fd_page_compact(ctypes.byref(desc), int(n_keep), _i32(seqlens, b, "seqlens"),
+                                   _i32(free_pages, desc.n_free_max, "free_pages"), _ptr(free_count),
+                                   _i32(block_table, b * desc.max_pages_per_seq, "block_table"), _i32(shares, desc.n_pages, "shares"),
+                                   _ptr(free_count_out), _i32(copy_src, lists, "copy_src"), _i32(copy_dst, lists, "copy_dst"),
                                    _ptr(copy_count), _stream(stream))
 
 
 def fd_page_copy(pools, copy_src, copy_dst, copy_count=None, n_pairs: int | None = None, stream=None) -> int:
     """Page copy_dst[i] of every pool (make_pools) becomes what page copy_src[i] is."""
     n = copy_src.numel() if n_pairs is None else int(n_pairs)
-    _ints("copy_src", copy_src, n)
-    _ints("copy_dst", copy_dst, n)
-    return _load().fd_page_copy(pools, len(pools), pools.n_pages, n, _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count),
-                                _stream(stream))
+    return _load().fd_page_copy(pools, len(pools), pools.n_pages, n, _i32(copy_src, n, "copy_src"), _i32(copy_dst, n, "copy_dst"),
+                                _ptr(copy_count), _stream(stream))
 
 
 def fd_device_status(stream=None, clear: bool = True) -> int:

@@ -148,7 +148,7 @@ def test_pages_refuse_counts(fd):
     assert page_call(fd, "trim", page_desc(fd, batch=8192, max_pages_per_seq=1 << 17, n_slots=8192)) == -2
     assert page_call(fd, "compact", page_desc(fd), n_keep=-1) == -1
     assert page_call(fd, "compact", page_desc(fd), n_keep=41) == -1
-    assert page_call(fd, "compact", page_desc(fd, n_pages=(1 << 22) + 30), n_keep=29) == -2
+    assert page_call(fd, "compact", page_desc(fd, n_pages=(1 << 19) + 30), n_keep=29) == -2
     assert page_call(fd, "trim", page_desc(fd), shares=A + 1) == -1
 
 
