@@ -978,6 +978,7 @@ fd_status fd_page_copy(const fd_pool* pools, int32_t n_pools, int32_t n_pages, i
         p.n_pools = n;
         p.n_pages = n_pages;
         p.n_pairs = n_pairs;
+        p.first = first == 0;
         p.src = copy_src;
         p.dst = copy_dst;
         p.count = copy_count;
