@@ -39,7 +39,6 @@ constexpr int kRopeWarps = 4;
 constexpr int kRopeCtas = 4;            // per SM
 constexpr int kRopeStages = 3;          // items of rows that a warp has in flight
 constexpr int kRopeGroups = 4;          // groups of four rows in an item
-constexpr int kPartsPerWarp = 2;        // a token is cut where that gives a warp fewer parts than these
 
 // inv_freq as a fraction of a turn per position, modulo 1, times 2^64.
 __device__ __forceinline__ uint64_t turns_of(float f) {
@@ -96,9 +95,8 @@ __device__ __forceinline__ uint2 quantised8(const float2* x, float inv) {
 }
 
 // An item is up to 4 GROUPS rows of one token: of its queries, its keys or its
-// values.  A warp takes `per_part` items of a token that follow each other (all of
-// them, where there are tokens enough), so that sines and cosines are computed
-// once for several; with more than one group, the rows of the items ahead are on
+// values.  The items of all tokens, in order, are dealt to the warps in equal runs, so
+// that sines and cosines are computed once for several; with more than one group, the rows of the items ahead are on
 // their way into the warp's stages of shared memory meanwhile (a bulk copy a row,
 // issued by a lane each, so that no register is spent on it).
 //
@@ -111,7 +109,7 @@ __device__ __forceinline__ uint2 quantised8(const float2* x, float inv) {
 // 4096 4.0); 53 % of the issue slots are taken.
 template <typename T, int GROUPS, bool PAIRS, bool F8, bool FULL>
 __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
-    fd_rope_kernel(const __grid_constant__ RopeParams p, int parts, int per_part) {
+    fd_rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr bool kStaged = GROUPS > 1;
     constexpr int kRows = 4 * GROUPS, kStageBytes = kRows * 256, kStages = kStaged ? kRopeStages : 1;
     extern __shared__ __align__(128) unsigned char s_rows[];    // [warps][stages][rows][256]
@@ -134,8 +132,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
     const int items_q = (p.side[0].heads + kRows - 1) / kRows, items_k = (p.side[1].heads + kRows - 1) / kRows;
     const int items = items_q + items_k + (p.side[2].cache != nullptr ? items_k : 0);
     const unsigned warps = gridDim.x * kRopeWarps, w0 = blockIdx.x * kRopeWarps + warp;
-    const unsigned dt = warps / parts, n_tokens = p.n_tokens;
-    const int dp = warps % parts;
+    const int64_t all = static_cast<int64_t>(p.n_tokens) * items;
+    const int64_t begin = all * w0 / warps;
+    int left = static_cast<int>(all * (w0 + 1) / warps - begin);   // items of this warp that are not done, and not asked for
+    int left_ahead = left;
     const uint32_t bars = smem_u32(s_bar[warp]);
     const uint32_t stages = smem_u32(s_rows) + warp * (kStages * kStageBytes);
     if constexpr (kStaged) {
@@ -146,23 +146,15 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
     grid_dependency_trigger();
     grid_dependency_wait();
 
-    struct Place {                      // an item of a token; t >= n_tokens: none
+    struct Place {                      // an item of a token
         unsigned t;
-        int part, i, end;
-    };
-    auto begin = [&](Place& x) {
-        x.i = x.part * per_part;
-        x.end = min(x.i + per_part, items);
+        int i;
     };
     auto advance = [&](Place& x) {
-        if (++x.i < x.end) return;
-        x.t += dt;
-        x.part += dp;
-        if (x.part >= parts) {
-            x.part -= parts;
+        if (++x.i == items) {
+            x.i = 0;
             ++x.t;
         }
-        begin(x);
     };
     auto kind_of = [&](const Place& x) { return x.i < items_q ? 0 : x.i < items_q + items_k ? 1 : 2; };
     auto first_of = [&](const Place& x, int kind) {
@@ -172,7 +164,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
     int64_t slot[kStages];
     uint4 direct[2];                    // (without stages: the item's rows)
     auto load = [&](const Place& x, int stage) {
-        if (x.t >= n_tokens) return;
+        if (left_ahead == 0) return;
+        --left_ahead;
         const int kind = kind_of(x), first = first_of(x, kind);
         const RopeSide& sd = p.side[kind];
         const int n = min(kRows, sd.heads - first);
@@ -189,8 +182,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
         slot[kStages - 1] = sd.cache != nullptr ? p.slots[x.t] : -1;
     };
 
-    Place cur = {w0 / parts, static_cast<int>(w0 % parts), 0, 0};
-    begin(cur);
+    Place cur = {static_cast<unsigned>(begin / items), static_cast<int>(begin % items)};
     Place ahead = cur;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
@@ -236,13 +228,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
         }
     };
     int stage = 0, phase = 0;
-    for (; cur.t < n_tokens; advance(cur)) {
+    for (; left > 0; --left, advance(cur)) {
         if (kStaged && !mbar_wait(bars + 8 * stage, phase)) {
             // the copies never came: say so, give those behind the same time, leave
             if (lane == 0) atomicOr(&g_status, kStatusTimeoutBit);
-            for (int s = 1; s < kStages; ++s) {
-                advance(cur);
-                if (cur.t >= n_tokens) break;
+            for (int s = 1; s < kStages && --left > 0; ++s) {
                 if (++stage == kStages) stage = 0, phase ^= 1;
                 mbar_wait(bars + 8 * stage, phase);
             }
@@ -402,13 +392,9 @@ cudaError_t launch_rope_v(const RopeParams& p, cudaStream_t stream) {
     static std::atomic<unsigned long long> configured_ctx{0};
     const cudaError_t e = allow_smem(kern, kSmem, configured_ctx);
     if (e != cudaSuccess) return e;
-    const int64_t warps = static_cast<int64_t>(sms) * kRopeCtas * kRopeWarps;
-    const int64_t want = std::min(items, (kPartsPerWarp * warps + p.n_tokens - 1) / p.n_tokens);
-    const int per_part = static_cast<int>((items + want - 1) / want);
-    const int parts = static_cast<int>((items + per_part - 1) / per_part);
-    const int64_t ctas = (static_cast<int64_t>(p.n_tokens) * parts + kRopeWarps - 1) / kRopeWarps;
+    const int64_t ctas = (static_cast<int64_t>(p.n_tokens) * items + kRopeWarps - 1) / kRopeWarps;
     return launch_pdl(kern, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms * kRopeCtas))), dim3(kRopeWarps * 32), kSmem,
-                      stream, p, parts, per_part);
+                      stream, p);
 }
 
 template <typename T, int GROUPS, bool PAIRS>
