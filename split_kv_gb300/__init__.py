@@ -278,7 +278,8 @@ _int32 = None
 
 
 def _i32(t, n: int, name: str):
-    """Address of n contiguous int32, checked if t is a tensor (addresses and None go unchecked)."""
+    """Address of n contiguous int32, checked if t is a tensor (addresses and None go unchecked, and
+    so do a call's tensors that its descriptor was made from: 0.8 us each)."""
     global _int32
     if t is None:
         return None
@@ -456,34 +457,34 @@ def fd_page_fork(desc: FdPageDesc, parents, children, keep, seqlens, free_pages,
                  free_count_out, copy_src, copy_dst, copy_count, n_forks: int | None = None, stream=None) -> int:
     """Sequences children[i] that share the pages of parents[i]'s first keep[i] tokens (None: of all)."""
     n = parents.numel() if n_forks is None else int(n_forks)
-    b, lists = desc.batch, desc.n_slots
+    b = desc.batch
     return _load().fd_page_fork(ctypes.byref(desc), n, _i32(parents, n, "parents"), _i32(children, n, "children"),
-                                _i32(keep, n, "keep"), _i32(seqlens, b, "seqlens"), _i32(free_pages, desc.n_free_max, "free_pages"),
-                                _ptr(free_count), _i32(block_table, b * desc.max_pages_per_seq, "block_table"),
+                                _i32(keep, n, "keep"), _i32(seqlens, b, "seqlens"), _ptr(free_pages),
+                                _ptr(free_count), _ptr(block_table),
                                 _i32(shares, desc.n_pages, "shares"), _i32(seqlens_out, b, "seqlens_out"), _ptr(free_count_out),
-                                _i32(copy_src, lists, "copy_src"), _i32(copy_dst, lists, "copy_dst"), _ptr(copy_count),
+                                _ptr(copy_src), _i32(copy_dst, desc.n_slots, "copy_dst"), _ptr(copy_count),
                                 _stream(stream))
 
 
 def fd_page_trim(desc: FdPageDesc, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out, free_count_out,
                  copy_src=None, copy_dst=None, copy_count=None, stream=None) -> int:
     """Sequences cut to their first keep[b] tokens; pages that nobody holds any more go back to the free stack."""
-    b, lists = desc.batch, desc.n_slots
+    b = desc.batch
     return _load().fd_page_trim(ctypes.byref(desc), _i32(keep, b, "keep"), _i32(seqlens, b, "seqlens"),
-                                _i32(free_pages, desc.n_free_max, "free_pages"), _ptr(free_count),
-                                _i32(block_table, b * desc.max_pages_per_seq, "block_table"), _i32(shares, desc.n_pages, "shares"),
-                                _i32(seqlens_out, b, "seqlens_out"), _ptr(free_count_out), _i32(copy_src, lists, "copy_src"),
-                                _i32(copy_dst, lists, "copy_dst"), _ptr(copy_count), _stream(stream))
+                                _ptr(free_pages), _ptr(free_count),
+                                _ptr(block_table), _i32(shares, desc.n_pages, "shares"),
+                                _i32(seqlens_out, b, "seqlens_out"), _ptr(free_count_out), _ptr(copy_src),
+                                _i32(copy_dst, desc.n_slots, "copy_dst"), _ptr(copy_count), _stream(stream))
 
 
 def fd_page_compact(desc: FdPageDesc, n_keep: int, seqlens, free_pages, free_count, block_table, shares, free_count_out,
                     copy_src, copy_dst, copy_count, stream=None) -> int:
     """Held pages from n_keep on renamed to free pages below it, for the high end of a pool to be given up."""
-    b, lists = desc.batch, desc.n_slots
+    b = desc.batch
     return _load().fd_page_compact(ctypes.byref(desc), int(n_keep), _i32(seqlens, b, "seqlens"),
-                                   _i32(free_pages, desc.n_free_max, "free_pages"), _ptr(free_count),
-                                   _i32(block_table, b * desc.max_pages_per_seq, "block_table"), _i32(shares, desc.n_pages, "shares"),
-                                   _ptr(free_count_out), _i32(copy_src, lists, "copy_src"), _i32(copy_dst, lists, "copy_dst"),
+                                   _ptr(free_pages), _ptr(free_count),
+                                   _ptr(block_table), _i32(shares, desc.n_pages, "shares"),
+                                   _ptr(free_count_out), _ptr(copy_src), _i32(copy_dst, desc.n_slots, "copy_dst"),
                                    _ptr(copy_count), _stream(stream))
 
 

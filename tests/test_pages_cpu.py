@@ -163,8 +163,8 @@ def test_pages_binding_refuses_sizes(fd):
     assert (d.batch, d.max_pages_per_seq, d.n_slots, d.n_free_max) == (3, 8, 3, 9)
     good = dict(keep=i(3), seqlens=i(3), free_pages=free, free_count=i(1), block_table=table, shares=i(9), seqlens_out=i(3), free_count_out=i(1),
                 copy_src=src, copy_dst=i(3), copy_count=i(1), stream=0)
-    for n, v in (("keep", i(2)), ("seqlens", i(3).long()), ("free_pages", i(8)), ("block_table", table.t()), ("shares", i(8)), ("seqlens_out", i(2)),
-                 ("copy_src", i(2)), ("copy_dst", i(3).float())):
+    for n, v in (("keep", i(2)), ("seqlens", i(3).long()), ("seqlens", i(6)[::2]), ("shares", i(8)), ("seqlens_out", i(2)), ("copy_dst", i(2)),
+                 ("copy_dst", i(3).float())):
         with pytest.raises(ValueError):
             fd.fd_page_trim(d, **{**good, n: v})
 
