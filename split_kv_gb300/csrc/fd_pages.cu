@@ -40,9 +40,9 @@ __device__ __forceinline__ int find(const int32_t* first, int n, int x) {
     return lo;
 }
 
-// Entries of the free stack; out of range counts raise a bit and are cut.
-__device__ __forceinline__ int free_entries(const PagePlanParams& p) {
-    const int count = *p.free_count;
+// Entries of the free stack, of the count as read; one out of range raises a bit and is cut.
+// (Apart from the read, whose latency other reads share.)
+__device__ __forceinline__ int free_entries(const PagePlanParams& p, int count) {
     if ((count < 0 || count > p.n_free_max) && blockIdx.x == 0 && threadIdx.x == 0) raise(kStatusSeqlenBit);
     return min(max(count, 0), p.n_free_max);
 }
@@ -96,12 +96,14 @@ __global__ void __launch_bounds__(1024) fd_page_fork_kernel(const PagePlanParams
     __shared__ long long s_sums[2][32];
     Scan scan{s_sums};
     const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.x;
+    // the last CTA writes what is one for all; the others (it too, if it is alone) copy rows
+    const bool scribe = rank == static_cast<int>(gridDim.x) - 1;
     const int ps1 = (1 << p.page_shift) - 1;
     const int64_t capacity = static_cast<int64_t>(p.max_pages) << p.page_shift;
     grid_dependency_trigger();
     grid_dependency_wait();
 
-    const int count = free_entries(p);
+    const int count_read = *p.free_count;
     for (int b = tid; b < p.batch; b += blockDim.x) s_owner[b] = s_lead[b] = INT32_MAX;
     __syncthreads();
     bool bad = false;
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(1024) fd_page_fork_kernel(const PagePlanParams
         s_add[i] = 0;
     }
     __syncthreads();
+    const int count = free_entries(p, count_read);
     int pages = 0, segments = 0;
     for (int base = 0; base < p.n_forks; base += blockDim.x) {
         const int i = base + tid;
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(1024) fd_page_fork_kernel(const PagePlanParams
             s_keep[i] = fits ? keep : -1;
             s_seg[i] = segments + low(upto) - segs;
             if (full > 0 && fits) atomicMin(&s_lead[from], i);
-            if (rank == 0 && (what & kForkRows) && part && fits) {
+            if (scribe && (what & kForkRows) && part && fits) {
                 const int src = p.block_table[static_cast<int64_t>(from) * p.max_pages + full];
                 const int dst = p.free_in[count - page_number];
                 if (src < 0 || src >= p.n_pages || dst < 0 || dst >= p.n_pages) raise(kStatusPageBit);
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(1024) fd_page_fork_kernel(const PagePlanParams
     if (tid == 0) s_seg[p.n_forks] = segments;
     __syncthreads();
     if (what & kForkRows) {
-        if (bad && rank == 0) raise(kStatusSeqlenBit);
+        if (bad && scribe) raise(kStatusSeqlenBit);
         for (int i = tid; i < p.n_forks; i += blockDim.x) {
             const int full = s_keep[i] >> p.page_shift;
             if (s_keep[i] < 0 || full == 0) continue;
@@ -161,8 +164,8 @@ __global__ void __launch_bounds__(1024) fd_page_fork_kernel(const PagePlanParams
             atomicAdd(&s_add[s_keep[lead] >> p.page_shift == full ? lead : i], 1);
         }
         __syncthreads();
-        const int warps = gridDim.x * (blockDim.x >> 5);
-        for (int s = rank * (blockDim.x >> 5) + (tid >> 5); s < segments; s += warps) {
+        const int warps = max(static_cast<int>(gridDim.x) - 1, 1) * (blockDim.x >> 5);
+        for (int s = scribe && gridDim.x > 1 ? segments : rank * (blockDim.x >> 5) + (tid >> 5); s < segments; s += warps) {
             const int i = find(s_seg, p.n_forks, s);
             const int j0 = (s - s_seg[i]) * kSegment, full = s_keep[i] >= 0 ? s_keep[i] >> p.page_shift : 0, add = s_add[i];
             const int32_t* from = p.block_table + static_cast<int64_t>(p.parents[i]) * p.max_pages;
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(1024) fd_page_fork_kernel(const PagePlanParams
             }
         }
     }
-    if (!(what & kForkFinish) || rank != 0) return;
+    if (!(what & kForkFinish) || !scribe) return;
     for (int b = tid; b < p.batch; b += blockDim.x) {
         const int i = s_owner[b];
         p.seqlens_out[b] = i != INT32_MAX && s_keep[i] >= 0 ? s_keep[i] : p.seqlens[b];
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
     grid_dependency_trigger();
     grid_dependency_wait();
 
-    const int count = free_entries(p);
+    const int count_read = *p.free_count;
     bool bad = false, bad_page = false;
     auto tail_page = [&](int b) {       // the page that a sequence keeps a part of, -1: none
         const int keep = s_keep[b];
@@ -240,6 +243,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
     };
     auto let_go = [&](int len, int keep) { return keep >= 0 ? ((len + ps1) >> p.page_shift) - ((keep + ps1) >> p.page_shift) : 0; };
     int claims = 0, E = 0;              // (E < 2^30, the host's check)
+    int my_len = 0;                     // of sequence tid
     for (int base = 0; base < p.batch; base += blockDim.x) {
         const int b = base + tid;
         int len = 0, keep = -1;
@@ -253,6 +257,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             if (keep >= len) keep = -1;
             keep = max(keep, -1);
             s_keep[b] = keep;
+            if (base == 0) my_len = len;
         }
         const int n = let_go(len, keep);
         long long all;
@@ -261,6 +266,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         claims += high(all);
         E += low(all);
     }
+    const int count = free_entries(p, count_read);
     __syncwarp();
     cluster_wait();
     if (claims > count) {
@@ -306,13 +312,14 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         for (int k = 0; k < kHeld; ++k) {
             const int e = first + 32 * k + lane;
             page[k] = -2;
+            if (first + 32 * k >= e1) break;
             if (e >= e1) continue;
             if (b < 0 || e >= s_first[b + 1]) b = find(s_first, p.batch, e);
             const int j = ((s_keep[b] + ps1) >> p.page_shift) + e - s_first[b];
             page[k] = p.block_table[static_cast<int64_t>(b) * p.max_pages + j];
         }
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
+        for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) {
             if (page[k] >= 0 && page[k] < p.n_pages) continue;
             bad_page |= first + 32 * k + lane < e1;
             page[k] = -1;
@@ -331,7 +338,9 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
     };
     // calls f(b, page) for the thread's claims
     const int b0 = rank * blockDim.x + tid;
-    int tail0 = b0 < p.batch ? tail_page(b0) : -1;
+    int tail0 = -1;                     // the first claim's page, read together with the references'
+    const bool claim0 = b0 < p.batch && s_keep[b0] >= 0 && (s_keep[b0] & ps1) != 0;
+    if (claim0) tail0 = p.block_table[static_cast<int64_t>(b0) * p.max_pages + (s_keep[b0] >> p.page_shift)];
     auto for_claims = [&](auto f) {
         if (tail0 >= 0) f(b0, tail0);
         for (int b = b0 + ranks * blockDim.x; b < p.batch; b += ranks * blockDim.x) {
@@ -340,6 +349,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         }
     };
     if (e0 < e1) load_pages(e0, held);
+    if (tail0 < 0 || tail0 >= p.n_pages) tail0 = -1;
     int given = 0;                      // references of this thread that give a page back
     bool any = false;
     if (shared) {
@@ -347,22 +357,26 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             any |= was != 0;
             if (left_of(was) < 0) raise(kStatusPageBit);      // let go more often than held
         };
-        for_claims([&](int, int page) { happened(atomicAdd(&p.shares[page], kEvent)); });
-        for_references([&](int, Pages& page) {
+        const int was0 = tail0 >= 0 ? atomicAdd(&p.shares[tail0], kEvent) : 0;
+        for_references([&](int first, Pages& page) {
             int was[kHeld];
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) was[k] = page[k] >= 0 ? atomicAdd(&p.shares[page[k]], kEvent) : 0;
+            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) was[k] = page[k] >= 0 ? atomicAdd(&p.shares[page[k]], kEvent) : 0;
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) {
+            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) {
                 happened(was[k]);
                 given += page[k] >= 0 && was[k] == 0;
             }
         });
+        happened(was0);
+        for_claims([&](int b, int page) {
+            if (b != b0) happened(atomicAdd(&p.shares[page], kEvent));
+        });
         for (int b = b0; b < p.batch; b += ranks * blockDim.x) bad_page |= s_keep[b] >= 0 && (s_keep[b] & ps1) != 0 && (b == b0 ? tail0 : tail_page(b)) < 0;
     } else {
-        for_references([&](int, Pages& page) {
+        for_references([&](int first, Pages& page) {
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) given += page[k] >= 0;
+            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) given += page[k] >= 0;
         });
     }
     long long cta_given;
@@ -380,15 +394,15 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         auto bid = [&](int number, int page, int word) {
             if (word != kEvent && (word <= -kCode || left_of(word) < 0)) atomicMin(&p.shares[page], code_of(number));
         };
-        auto words_of = [&](const Pages& page, Pages& word) {
+        auto words_of = [&](int first, const Pages& page, Pages& word) {
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) word[k] = page[k] >= 0 ? __ldcg(p.shares + page[k]) : 0;
+            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) word[k] = page[k] >= 0 ? __ldcg(p.shares + page[k]) : 0;
         };
         for_references([&](int first, Pages& page) {
             Pages word;
-            words_of(page, word);
+            words_of(first, page, word);
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k)
+            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k)
                 if (page[k] >= 0) bid(first + 32 * k + lane, page[k], word[k]);
         });
         for_claims([&](int b, int page) { bid(E + b, page, __ldcg(p.shares + page)); });
@@ -396,9 +410,9 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         given = 0;
         for_references([&](int first, Pages& page) {
             Pages word;
-            words_of(page, word);
+            words_of(first, page, word);
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) given += page[k] >= 0 && (word[k] == kEvent || word[k] == code_of(first + 32 * k + lane));
+            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) given += page[k] >= 0 && (word[k] == kEvent || word[k] == code_of(first + 32 * k + lane));
         });
         upto = scan(given, cta_given);
         if (tid < ranks) remote_store(remote_smem(smem_u32(&s_given[rank]), tid), static_cast<uint32_t>(low(cta_given)));
@@ -432,6 +446,13 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         all_given += static_cast<int>(s_given[r]);
     }
     const int base = count - taken;
+    if (rank == 0) {
+        for (int b = tid; b < p.batch; b += blockDim.x) p.seqlens_out[b] = s_keep[b] >= 0 ? s_keep[b] : b == tid ? my_len : p.seqlens[b];
+        if (tid == 0) {
+            *p.free_count_out = static_cast<int>(min(static_cast<int64_t>(base) + all_given, static_cast<int64_t>(p.n_free_max)));
+            if (p.copy_count != nullptr) *p.copy_count = taken;
+        }
+    }
     // whether the event decides for the page; its word is made a count again
     auto settle = [&](int number, int page, int word) {
         const bool mine = word == kEvent || word == code_of(number);
@@ -448,9 +469,9 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
     for_references([&](int first, Pages& page) {
         Pages word;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) word[k] = others != 0 && page[k] >= 0 ? __ldcg(p.shares + page[k]) : kEvent;
+        for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) word[k] = others != 0 && page[k] >= 0 ? __ldcg(p.shares + page[k]) : kEvent;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
+        for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) {
             bool mine = page[k] >= 0;
             if (mine && shared) mine = settle(first + 32 * k + lane, page[k], word[k]);
             const unsigned votes = __ballot_sync(kFullMask, mine);
@@ -463,12 +484,6 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         }
     });
     if (bad_page) raise(kStatusPageBit);
-    if (rank != 0) return;
-    for (int b = tid; b < p.batch; b += blockDim.x) p.seqlens_out[b] = s_keep[b] >= 0 ? s_keep[b] : p.seqlens[b];
-    if (tid == 0) {
-        *p.free_count_out = static_cast<int>(min(static_cast<int64_t>(base) + all_given, static_cast<int64_t>(p.n_free_max)));
-        if (p.copy_count != nullptr) *p.copy_count = taken;
-    }
 }
 
 // ---------------------------------------------------------------- compaction
@@ -503,13 +518,13 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
     grid_dependency_wait();
 
     const int warps = ranks * (threads >> 5), w0 = rank * (threads >> 5) + warp;
-    const int count = free_entries(p);
+    const int count_read = *p.free_count;
     int entry[kEntries];
     auto load_entries = [&](int64_t base) {
 #pragma unroll
         for (int k = 0; k < kEntries; ++k) {
             const int64_t i = base + static_cast<int64_t>(w0) * (32 * kEntries) + 32 * k + lane;
-            entry[k] = i < count ? min(p.free_pages[i], INT32_MAX - 1) : kNothing;
+            entry[k] = i < p.n_free_max ? p.free_pages[i] : 0;     // (not looked at here: other reads share the latency)
         }
     };
     load_entries(0);
@@ -577,12 +592,15 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
         mark(page);
     }
     // the entries of the free stack that stay in it or are used up
+    const int count = free_entries(p, count_read);
     int kept = 0, at = 0;               // of the rounds before; where this warp's go
     unsigned votes[kEntries];
-    auto count_entries = [&](uint32_t* counts) {
+    auto count_entries = [&](int64_t base, uint32_t* counts) {
         int n = 0;
 #pragma unroll
         for (int k = 0; k < kEntries; ++k) {
+            const int64_t i = base + static_cast<int64_t>(w0) * (32 * kEntries) + 32 * k + lane;
+            entry[k] = i < count ? min(entry[k], INT32_MAX - 1) : kNothing;
             if (entry[k] < 0 || (entry[k] >= p.n_pages && entry[k] != kNothing)) raise(kStatusPageBit);
             votes[k] = __ballot_sync(kFullMask, entry[k] >= 0 && entry[k] < p.n_keep);
             n += __popc(votes[k]);
@@ -603,7 +621,7 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
             at += __popc(votes[k]);
         }
     };
-    count_entries(s_kept[0]);
+    count_entries(0, s_kept[0]);
     cluster_barrier();              // the maps are marked, and every CTA has read its entries
 
     write_entries(s_kept[0]);
@@ -611,7 +629,7 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
     int turn = 1;
     for (int64_t base = round; base < count; base += round, turn ^= 1) {
         load_entries(base);
-        count_entries(s_kept[turn]);
+        count_entries(base, s_kept[turn]);
         cluster_barrier();
         write_entries(s_kept[turn]);
     }
@@ -708,7 +726,7 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
     }
 }
 
-// One cluster of `ctas` CTAs.
+// One cluster of `ctas` CTAs (more than 8 are allowed once per context, like shared memory).
 template <typename Kern, typename... Args>
 cudaError_t launch_cluster(Kern kern, int ctas, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
@@ -726,7 +744,14 @@ cudaError_t launch_cluster(Kern kern, int ctas, int threads, size_t smem, cudaSt
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     cudaError_t e = cudaSuccess;
-    if (ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);   // (idempotent)
+    if (ctas > 8) {
+        static std::atomic<unsigned long long> configured_ctx{0};
+        const unsigned long long ctx = current_context_id();
+        if (ctx == 0 || configured_ctx.load(std::memory_order_acquire) != ctx) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess && ctx != 0) configured_ctx.store(ctx, std::memory_order_release);
+        }
+    }
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -747,7 +772,7 @@ cudaError_t launch_page_fork(const PagePlanParams& p, cudaStream_t stream) {
     // a warp for each segment that the rows can have
     const int64_t segments = static_cast<int64_t>(p.n_forks) * ((p.max_pages + kSegment - 1) / kSegment);
     const int64_t want = (segments + threads / 32 - 1) / (threads / 32);
-    const int ctas = static_cast<int>(want < 1 ? 1 : want < sms ? want : sms);
+    const int ctas = want <= 1 ? 1 : static_cast<int>(want < sms ? want + 1 : sms);
     // lengths or the count in place: they are written when every CTA has read them
     const bool in_place = p.seqlens == p.seqlens_out || p.free_count == p.free_count_out;
     if (ctas == 1 || !in_place) return launch_pdl(fd_page_fork_kernel, dim3(ctas), dim3(threads), smem, stream, p, kForkRows | kForkFinish);
