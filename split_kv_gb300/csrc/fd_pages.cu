@@ -726,9 +726,10 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
     }
 }
 
-// One cluster of `ctas` CTAs (more than 8 are allowed once per context, like shared memory).
+// One cluster of `ctas` CTAs; more than 8 have to be allowed, once per context (large_ctx: the kernel's own).
 template <typename Kern, typename... Args>
-cudaError_t launch_cluster(Kern kern, int ctas, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+cudaError_t launch_cluster(Kern kern, std::atomic<unsigned long long>& large_ctx, int ctas, int threads, size_t smem,
+                           cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
@@ -745,11 +746,10 @@ cudaError_t launch_cluster(Kern kern, int ctas, int threads, size_t smem, cudaSt
     cfg.numAttrs = 2;
     cudaError_t e = cudaSuccess;
     if (ctas > 8) {
-        static std::atomic<unsigned long long> configured_ctx{0};
         const unsigned long long ctx = current_context_id();
-        if (ctx == 0 || configured_ctx.load(std::memory_order_acquire) != ctx) {
+        if (ctx == 0 || large_ctx.load(std::memory_order_acquire) != ctx) {
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess && ctx != 0) configured_ctx.store(ctx, std::memory_order_release);
+            if (e == cudaSuccess && ctx != 0) large_ctx.store(ctx, std::memory_order_release);
         }
     }
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, args...);
@@ -781,21 +781,22 @@ cudaError_t launch_page_fork(const PagePlanParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_page_trim(const PagePlanParams& p, cudaStream_t stream) {
-    static std::atomic<unsigned long long> configured_ctx{0};
+    static std::atomic<unsigned long long> configured_ctx{0}, large_ctx{0};
     cudaError_t e = allow_smem(fd_page_trim_kernel, (3 * FD_MAX_TABLE_BATCH + 1) * sizeof(int32_t), configured_ctx);
     if (e != cudaSuccess) return e;
     const size_t smem = (3 * static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
     // Eight CTAs of 256 threads while a thread cannot get more than 16 references, else as
-    // many as a cluster has, of 512.  Drafts of 64 sequences / 37600 references (with pages
-    // of six, 43 sequences ending in one), us: 8 x 128 7.0 / 75, 8 x 256 7.1 / 45, 8 x 512 7.3 / 33,
-    // 16 x 256 7.2 / 29, 16 x 512 7.5 / 19, 16 x 768 7.9 / 21.
+    // many as a cluster has, of 512.  Drafts of 64 sequences / 37600 references (pages of six
+    // sequences among them, parts of which others keep), us with the copy that restores the
+    // state (1.3): 8 x 128 7.0 / 75, 8 x 256 7.1 / 45, 8 x 512 7.3 / 33, 16 x 256 7.2 / 29, 16 x 512 7.5 / 19,
+    // 16 x 768 7.9 / 21; since a warp's loops end where its references do, 8 x 256 6.1, 16 x 512 19.
     const bool small = static_cast<int64_t>(p.batch) * p.max_pages <= 16 * 8 * 256;
-    return launch_cluster(fd_page_trim_kernel, small ? 8 : kMaxCtas, small ? 256 : 512, smem, stream, p);
+    return launch_cluster(fd_page_trim_kernel, large_ctx, small ? 8 : kMaxCtas, small ? 256 : 512, smem, stream, p);
 }
 
 cudaError_t launch_page_compact(const PagePlanParams& p, cudaStream_t stream) {
     constexpr int kMaxWords = FD_MAX_COMPACT_PAGES / 32 + kMaxCtas;
-    static std::atomic<unsigned long long> configured_ctx{0};
+    static std::atomic<unsigned long long> configured_ctx{0}, large_ctx{0};
     cudaError_t e = allow_smem(fd_page_compact_kernel, (2 * FD_MAX_TABLE_BATCH + 1 + 2 * kMaxWords) * sizeof(int32_t), configured_ctx);
     if (e != cudaSuccess) return e;
     // As many threads as hold tables and free stack in registers, within a cluster's.
@@ -806,7 +807,7 @@ cudaError_t launch_page_compact(const PagePlanParams& p, cudaStream_t stream) {
     const int64_t words = (static_cast<int64_t>(p.n_pages) - p.n_keep + 31) / 32;
     const int words_per_cta = static_cast<int>(words < ctas ? 1 : (words + ctas - 1) / ctas);
     const size_t smem = (2 * static_cast<size_t>(p.batch) + 1 + 2 * static_cast<size_t>(words_per_cta) * ctas) * sizeof(int32_t);
-    return launch_cluster(fd_page_compact_kernel, ctas, small ? 128 : 512, smem, stream, p, words_per_cta);
+    return launch_cluster(fd_page_compact_kernel, large_ctx, ctas, small ? 128 : 512, smem, stream, p, words_per_cta);
 }
 
 cudaError_t status_word_pages(unsigned** word) {
