@@ -502,8 +502,8 @@ fd_status fd_prompt(const fd_prompt_desc* desc, const void* q, const void* k, co
  * Both, and fd_page_compact, write down what has to be copied as a list:
  * copy_src[i] -> copy_dst[i], i < *copy_count (device int32[n_slots] and
  * int32[1]; entries behind are left as they are), which fd_page_copy carries out
- * in the caches of every layer, before anything is appended.  No page is in a
- * list as a source and as a destination.
+ * in the caches of every layer, before anything is appended and before the next
+ * list is made.  No page is in a list as a source and as a destination.
  * ====================================================================== */
 
 #define FD_NORM_Q 1     /* fd_rope_desc.norm: queries */
@@ -588,9 +588,9 @@ fd_status fd_qkv_rope(const fd_rope_desc* desc, const void* q, const void* k, co
  *  shares        : device int32[n_pages], in and out.
  * All parents are read as they were before the call.  A fork out of range (an index
  * outside the batch, a child that is its own parent, holds tokens already or is
- * named by an earlier valid fork, keep < 0 or beyond the parent's tokens) or whose page the
- * free list cannot cover in that order is left out: its child stays as it was.
- * Those, a page index outside the pool, and a free count out of range set
+ * named by an earlier fork that is in range, keep < 0 or beyond the parent's
+ * tokens) or whose page the free list cannot cover in that order is left out: its
+ * child stays as it was.  Those, a page index outside the pool, and a free count out of range set
  * FD_ERR_DEVICE_BOUNDS in the status word. */
 fd_status fd_page_fork(const fd_page_desc* desc, int32_t n_forks, const int32_t* parents,
                        const int32_t* children, const int32_t* keep, const int32_t* seqlens,
@@ -670,7 +670,7 @@ typedef struct fd_pool {
  * A pair with a negative index, or of a page with itself, is left out; so is one with an
  * index beyond the pool, which sets FD_ERR_DEVICE_BOUNDS in the status word.  A page
  * may be the source of many pairs; one that is a destination is in no other pair
- * (else what it and they get is unspecified). */
+ * (else what it and they get is unspecified).  No two pools share memory. */
 fd_status fd_page_copy(const fd_pool* pools, int32_t n_pools, int32_t n_pages, int32_t n_pairs,
                        const int32_t* copy_src, const int32_t* copy_dst, const int32_t* copy_count,
                        void* stream);

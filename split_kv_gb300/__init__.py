@@ -274,25 +274,28 @@ def _check_scales(desc, scales: FdKvScales) -> None:
         raise ValueError(f"scales {scales.shape} of {scales.block}-token blocks do not cover the cache")
 
 
-_int32 = None
+_types = {}
 
 
-def _i32(t, n: int, name: str):
-    """Address of n contiguous int32, checked if t is a tensor (addresses and None go unchecked, and
-    so do a call's tensors that its descriptor was made from: 0.8 us each)."""
-    global _int32
+def _array(t, n: int, name: str, kind: str):
+    """Address of n contiguous elements of the type, checked if t is a tensor (addresses and None go
+    unchecked, and so do a call's tensors that its descriptor was made from: 0.8 us each)."""
     if t is None:
         return None
     try:
         dtype = t.dtype
-        if _int32 is None:
-            import torch
-            _int32 = torch.int32
-        if dtype is not _int32 or t.nbytes < 4 * n or not t.is_contiguous():
-            raise ValueError(f"{name} must be {n} contiguous int32")
-        return t.data_ptr()
     except AttributeError:
         return _ptr(t)
+    if not _types:
+        import torch
+        _types.update(int32=torch.int32, int64=torch.int64, float32=torch.float32)
+    if dtype is not _types[kind] or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {kind}")
+    return t.data_ptr()
+
+
+def _i32(t, n: int, name: str):
+    return _array(t, n, name, "int32")
 
 
 def check(status: int, what: str = "") -> int:
@@ -438,19 +441,9 @@ def fd_qkv_rope(desc: FdRopeDesc, q, k, v, q_weight, k_weight, inv_freq, positio
                 v_cache, stream=None) -> int:
     """Norms and rotation of a step's queries and keys, and the way of its keys and values into a cache."""
     n = desc.n_tokens
-    pos = _i32(positions, n, "positions")
-    try:
-        if inv_freq is not None and (inv_freq.nbytes < 2 * desc.rot_dim or inv_freq.element_size() != 4 or not inv_freq.is_contiguous()):
-            raise ValueError(f"inv_freq must be {desc.rot_dim // 2} contiguous float32")
-    except AttributeError:
-        pass
-    try:
-        if slots is not None and (slots.element_size() != 8 or slots.nbytes < 8 * n or not slots.is_contiguous()):
-            raise ValueError(f"slots must be {n} contiguous int64")
-    except AttributeError:
-        pass
-    return _load().fd_qkv_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-                               pos, _ptr(slots), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _stream(stream))
+    return _load().fd_qkv_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
+                               _array(inv_freq, desc.rot_dim // 2, "inv_freq", "float32"), _array(positions, n, "positions", "int32"),
+                               _array(slots, n, "slots", "int64"), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _stream(stream))
 
 
 def fd_page_fork(desc: FdPageDesc, parents, children, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out,

@@ -427,7 +427,9 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             taken += low(all);
             if (base / static_cast<int>(blockDim.x) % ranks != rank || b >= p.batch) continue;   // (b is a claim of this very thread)
             s_new[b] = kNone;
-            if (moves) {
+            if (moves && number > count) {      // (shares that were less than the holders: the page stays as it is)
+                raise(kStatusPageBit);
+            } else if (moves) {
                 const int to = p.free_in[count - number];
                 if (to < 0 || to >= p.n_pages) raise(kStatusPageBit);
                 p.copy_src[number - 1] = page;
@@ -435,6 +437,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
                 s_new[b] = to;
             }
         }
+        taken = min(taken, count);
         cluster_barrier();
     }
     // where this warp's pages go: behind those of the CTAs and warps before it

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
     };
     int stage = 0, phase = 0;
     for (; left > 0; --left, advance(cur)) {
-        if (kStaged && !mbar_wait(bars + 8 * stage, phase)) {
+        if (kStaged && __any_sync(kFullMask, !mbar_wait(bars + 8 * stage, phase))) {
             // the copies never came: say so, give those behind the same time, leave
             if (lane == 0) atomicOr(&g_status, kStatusTimeoutBit);
             for (int s = 1; s < kStages && --left > 0; ++s) {

@@ -251,6 +251,42 @@ def test_trim(batch, page, width, n, alias):
     assert want["count"] == s.n_pages and not any(want["shares"]) and sorted(want["free"][:s.n_pages]) == list(range(s.n_pages))
 
 
+@pytest.mark.parametrize("batch,width", [(64, 500), (64, 2600)])
+def test_trim_of_more_than_a_threads_registers_hold(batch, width):
+    s = State(batch + width, batch, 16, width, held=1.0, spare=batch * 3 + 20)
+    s.lens[batch - 1] = 0
+    for keep in ([0] * batch, [x // 7 for x in s.lens]):
+        want, bad = want_trim(s, keep, False)
+        assert not bad
+        same(run_trim(s, keep, shared=False), want)
+    # half of the sequences become forks of a long one
+    long = max(range(batch), key=lambda b: s.lens[b])
+    children = [b for b in range(1, batch, 2) if b != long]
+    for b in children:
+        s.lens[b], s.table[b] = 0, [-9] * width
+    out, bad = want_fork(s, [long] * len(children), children, [s.lens[long] - (b * 31) % 200 for b in children])
+    assert not bad
+    s.take(out)
+    keep = [x if b % 3 else x // 5 for b, x in enumerate(s.lens)]
+    want, bad = want_trim(s, keep)
+    assert not bad
+    same(run_trim(s, keep), want)
+
+
+@pytest.mark.parametrize("count", [0, 1, 3, 30])
+def test_trim_over_counts_that_are_too_low(count):
+    """Eight sequences that end inside one page of which shares knows nothing: reported, within bounds."""
+    s = State(3, 8, 16, 6, held=1.0, spare=40)
+    s.lens = [40] * 8
+    s.table = [[1, 2, 3, -9, -9, -9] for _ in range(8)]
+    s.n_pages, s.shares = 40, [0] * 40
+    s.free, s.count = list(range(4, 40)) + [-5] * 4, count
+    t = run_trim(s, [20] * 8)
+    assert fd.fd_device_status(clear=True) == fd.FD_ERR_DEVICE_BOUNDS
+    assert 0 <= int(t["count_out"]) <= 40 and 0 <= int(t["n"]) <= count
+    assert all(0 <= x < 40 for row in t["table"].tolist() for x in row[:3]) and t["lens_out"].tolist() == [20] * 8
+
+
 @pytest.mark.parametrize("batch,page,width,n", SIZES)
 def test_trim_without_shares(batch, page, width, n):
     s = State(batch * 3 + page, batch, page, width)
@@ -345,6 +381,14 @@ def test_compact_a_large_pool():
         want, bad = want_compact(s, n_keep, s.n_pages)
         assert bad == (n_keep == 1000)
         same(run_compact(s, n_keep, s.n_pages), want, bad)
+
+
+def test_compact_of_many_segments():
+    s = State(23, 200, 16, 1100, held=1.0, spare=30000)
+    for n_keep in (s.n_pages - s.count + 5000, s.n_pages - s.count):
+        want, bad = want_compact(s, n_keep, s.n_pages)
+        assert not bad and want["n"] > 10000
+        same(run_compact(s, n_keep, s.n_pages), want)
 
 
 @pytest.mark.parametrize("what", ["bad length", "bad page", "bad free page", "free count"])
@@ -517,6 +561,43 @@ def test_page_operators_captured():
         assert t["table"].tolist() == out["table"] and t["shares"].tolist() == out["shares"] and int(count3) == out["count"]
         assert lens2.tolist() == n.lens and t["free"].tolist() == out["free"] and int(t["n"]) == out["n"]
         assert torch.equal(bits(cache), bits(want))
+
+
+def test_copies_of_several_shapes_captured():
+    """Launches of one call that overlap each other still come behind what wrote the list and the pages,
+    and before what reads them."""
+    P = 300
+    pools = [rand_bytes(20, torch.bfloat16, P, 8, 16, 128), rand_bytes(21, torch.float32, P, 8, 2), rand_bytes(22, torch.bfloat16, P, 2, 8, 128),
+             rand_bytes(23, torch.uint8, P, 5, 3)]
+    first = [x.clone() for x in pools]
+    src, dst, n = i32([0] * 100), i32([0] * 100), i32([0])
+    given = [i32([0] * 100), i32([0] * 100), i32([0])]
+    handle = fd.make_pools(pools)
+    after = [torch.empty_like(x) for x in pools]
+
+    def step():
+        for x, y in zip(pools, first):
+            bits(x).copy_(bits(y))
+        for x, y in zip((src, dst, n), given):
+            x.copy_(y)
+        fd.check(fd.fd_page_copy(handle, src, dst, n))
+        for x, y in zip(after, pools):
+            bits(x).copy_(bits(y))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(5):
+        perm = [int(x) for x in np.random.default_rng(seed).permutation(P)]
+        m = 100 - seed * 20
+        for x, v in zip(given, (perm[:100], perm[100:200], [m])):
+            x.copy_(i32(v))
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(after, first):
+            assert torch.equal(bits(x), bits(copied(y, list(zip(perm[:100], perm[100:200]))[:m])))
 
 
 def test_two_streams_at_once():

@@ -88,7 +88,7 @@ def test_rope_binding_refuses_sizes(fd):
     d = fd.make_rope_desc(x, x, q_out=x, k_out=x)
     i, f, s = torch.zeros(3, dtype=torch.int32), torch.zeros(64), torch.zeros(3, dtype=torch.int64)
     for pos, freq, slots in ((i[:2], f, s), (i.long(), f, s), (i.float(), f, s), (i, f[:63], s), (i, f.double(), s), (i, f, s[:2]),
-                             (i, f, i), (i, f[::2], s)):
+                             (i, f, i), (i, torch.zeros(128)[::2], s), (i, f.int(), s), (i, f, s.double())):
         with pytest.raises(ValueError):
             fd.fd_qkv_rope(d, x, x, None, None, None, freq, pos, slots, x, x, None, None, 0)
     bad = [dict(q=x, k=x.to(torch.bfloat16), q_out=x, k_out=x), dict(q=x, k=x, q_out=x[:2], k_out=x), dict(q=x, k=x, q_out=x),
