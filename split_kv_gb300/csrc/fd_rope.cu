@@ -32,9 +32,10 @@ __device__ unsigned int g_status = 0;   // this file's bits of the device status
 
 constexpr unsigned kFullMask = 0xffffffffu;
 // 4 warps of 128 registers in 4 CTAs an SM, 3 stages of 16 rows (4 KB) each: 192 KB
-// of rows on their way.  16384 tokens, 32 / 8 heads, bf16, into a cache (403 MB): 71.5 us, 5.6
-// TB/s; 12 warps an SM with 4 stages 76, 20 with 8-row stages 120 (spills); all
-// rows through registers instead, 2 / 3 / 4 groups ahead, 96 / 105 / 125.
+// of rows on their way.  16384 tokens, 32 / 8 heads, bf16, into a cache (403 MB): 68.7 us, 5.9
+// TB/s.  By the way there: 12 warps an SM with 4 stages 76 against 71.5, 20 with 8-row
+// stages 120 (spills); all rows through registers instead, 2 / 3 / 4 groups
+// ahead, 96 / 105 / 125; two groups' sums and roots side by side, no change.
 constexpr int kRopeWarps = 4;
 constexpr int kRopeCtas = 4;            // per SM
 constexpr int kRopeStages = 3;          // items of rows that a warp has in flight
@@ -105,8 +106,8 @@ __device__ __forceinline__ uint2 quantised8(const float2* x, float inv) {
 // instruction.  FULL: whole rows are rotated; else the elements that
 // are not never meet their B (an infinity times 0 would be a NaN).
 //
-// Large calls are bound by HBM and by their ends (65536 tokens 6.3 TB/s, 16384 5.6,
-// 4096 4.0); 53 % of the issue slots are taken.
+// Large calls are bound by HBM and by their ends (65536 tokens 6.2 TB/s, 16384 5.9, 4096
+// 5.0): a plain copy of the same 403 MB takes about 65 us.  56 % of the issue slots are taken.
 template <typename T, int GROUPS, bool PAIRS, bool F8, bool FULL>
 __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
     fd_rope_kernel(const __grid_constant__ RopeParams p) {
@@ -136,6 +137,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
     const int64_t begin = all * w0 / warps;
     int left = static_cast<int>(all * (w0 + 1) / warps - begin);   // items of this warp that are not done, and not asked for
     int left_ahead = left;
+    // Heads that lie end to end may come in one copy, which starts sooner, or in one a row, which
+    // keeps more of them on their way.  A row / one, us: 32 / 8 heads, 1024 tokens 6.9 / 6.2, 4096
+    // 20.7 / 20.2, 16384 68.7 / 71.4; 8 / 8 heads, 2048 7.0 / 6.4; 64 / 8, 8192 58.3 / 62.5.
+    const bool few = all <= 8 * static_cast<int64_t>(warps);
     const uint32_t bars = smem_u32(s_bar[warp]);
     const uint32_t stages = smem_u32(s_rows) + warp * (kStages * kStageBytes);
     if constexpr (kStaged) {
@@ -172,7 +177,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
         const T* src = static_cast<const T*>(sd.src) + x.t * sd.src_t;
         if constexpr (kStaged) {
             if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, n * 256);
-            if (lane < n) bulk_load(stages + stage * kStageBytes + lane * 256, src + (first + lane) * sd.src_h, 256, bars + 8 * stage);
+            const bool dense = few && sd.src_h == kHeadDim;
+            if (lane < (dense ? 1 : n))
+                bulk_load(stages + stage * kStageBytes + lane * 256, src + (first + lane) * sd.src_h, dense ? n * 256 : 256, bars + 8 * stage);
         } else {
             const uint4* row = reinterpret_cast<const uint4*>(src + (first + min(sub, n - 1)) * sd.src_h);
             direct[0] = row[c0];
