@@ -305,11 +305,11 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
     const int e0 = min(static_cast<int64_t>(rank * (blockDim.x >> 5) + warp) * per_warp, static_cast<int64_t>(E));
     const int e1 = min(e0 + per_warp, E);
     // the pages of the thread's references first + 32 k + lane, -1 behind the warp's last or outside the pool
-    using Pages = int[kHeld];
-    auto load_pages = [&](int first, Pages& page) {
+    auto load_pages = [&](int first, auto& page) {
+        constexpr int K = sizeof(page) / sizeof(int);
         int b = -1;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
+        for (int k = 0; k < K; ++k) {
             const int e = first + 32 * k + lane;
             page[k] = -2;
             if (first + 32 * k >= e1) break;
@@ -319,19 +319,20 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             page[k] = p.block_table[static_cast<int64_t>(b) * p.max_pages + j];
         }
 #pragma unroll
-        for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) {
+        for (int k = 0; k < K && first + 32 * k < e1; ++k) {
             if (page[k] >= 0 && page[k] < p.n_pages) continue;
             bad_page |= first + 32 * k + lane < e1;
             page[k] = -1;
         }
     };
-    // calls f(first, pages) for the warp's references, kHeld a thread at a time; the
-    // first ones' pages stay in registers from phase to phase
-    Pages held;
+    // calls f(first, pages) for the warp's references: the first kHeld of a thread at once,
+    // whose pages stay in registers from phase to phase, others one by one
+    int held[kHeld];
     auto for_references = [&](auto f) {
         if (e0 < e1) f(e0, held);
-        for (int first = e0 + 32 * kHeld; first < e1; first += 32 * kHeld) {
-            Pages page;
+#pragma unroll 1
+        for (int first = e0 + 32 * kHeld; first < e1; first += 32) {
+            int page[1];
             load_pages(first, page);
             f(first, page);
         }
@@ -358,12 +359,13 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             if (left_of(was) < 0) raise(kStatusPageBit);      // let go more often than held
         };
         const int was0 = tail0 >= 0 ? atomicAdd(&p.shares[tail0], kEvent) : 0;
-        for_references([&](int first, Pages& page) {
-            int was[kHeld];
+        for_references([&](int first, auto& page) {
+            constexpr int K = sizeof(page) / sizeof(int);
+            int was[K];
 #pragma unroll
-            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) was[k] = page[k] >= 0 ? atomicAdd(&p.shares[page[k]], kEvent) : 0;
+            for (int k = 0; k < K && first + 32 * k < e1; ++k) was[k] = page[k] >= 0 ? atomicAdd(&p.shares[page[k]], kEvent) : 0;
 #pragma unroll
-            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) {
+            for (int k = 0; k < K && first + 32 * k < e1; ++k) {
                 happened(was[k]);
                 given += page[k] >= 0 && was[k] == 0;
             }
@@ -374,9 +376,10 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         });
         for (int b = b0; b < p.batch; b += ranks * blockDim.x) bad_page |= s_keep[b] >= 0 && (s_keep[b] & ps1) != 0 && (b == b0 ? tail0 : tail_page(b)) < 0;
     } else {
-        for_references([&](int first, Pages& page) {
+        for_references([&](int first, auto& page) {
+            constexpr int K = sizeof(page) / sizeof(int);
 #pragma unroll
-            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) given += page[k] >= 0;
+            for (int k = 0; k < K && first + 32 * k < e1; ++k) given += page[k] >= 0;
         });
     }
     long long cta_given;
@@ -394,25 +397,28 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         auto bid = [&](int number, int page, int word) {
             if (word != kEvent && (word <= -kCode || left_of(word) < 0)) atomicMin(&p.shares[page], code_of(number));
         };
-        auto words_of = [&](int first, const Pages& page, Pages& word) {
+        auto words_of = [&](int first, auto& page, auto& word) {
+            constexpr int K = sizeof(page) / sizeof(int);
 #pragma unroll
-            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) word[k] = page[k] >= 0 ? __ldcg(p.shares + page[k]) : 0;
+            for (int k = 0; k < K && first + 32 * k < e1; ++k) word[k] = page[k] >= 0 ? __ldcg(p.shares + page[k]) : 0;
         };
-        for_references([&](int first, Pages& page) {
-            Pages word;
+        for_references([&](int first, auto& page) {
+            constexpr int K = sizeof(page) / sizeof(int);
+            int word[K];
             words_of(first, page, word);
 #pragma unroll
-            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k)
+            for (int k = 0; k < K && first + 32 * k < e1; ++k)
                 if (page[k] >= 0) bid(first + 32 * k + lane, page[k], word[k]);
         });
         for_claims([&](int b, int page) { bid(E + b, page, __ldcg(p.shares + page)); });
         cluster_barrier();
         given = 0;
-        for_references([&](int first, Pages& page) {
-            Pages word;
+        for_references([&](int first, auto& page) {
+            constexpr int K = sizeof(page) / sizeof(int);
+            int word[K];
             words_of(first, page, word);
 #pragma unroll
-            for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) given += page[k] >= 0 && (word[k] == kEvent || word[k] == code_of(first + 32 * k + lane));
+            for (int k = 0; k < K && first + 32 * k < e1; ++k) given += page[k] >= 0 && (word[k] == kEvent || word[k] == code_of(first + 32 * k + lane));
         });
         upto = scan(given, cta_given);
         if (tid < ranks) remote_store(remote_smem(smem_u32(&s_given[rank]), tid), static_cast<uint32_t>(low(cta_given)));
@@ -469,12 +475,13 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             if (others != 0 && s_new[b] != kNone)
                 p.block_table[static_cast<int64_t>(b) * p.max_pages + (s_keep[b] >> p.page_shift)] = s_new[b];
         });
-    for_references([&](int first, Pages& page) {
-        Pages word;
+    for_references([&](int first, auto& page) {
+            constexpr int K = sizeof(page) / sizeof(int);
+        int word[K];
 #pragma unroll
-        for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) word[k] = others != 0 && page[k] >= 0 ? __ldcg(p.shares + page[k]) : kEvent;
+        for (int k = 0; k < K && first + 32 * k < e1; ++k) word[k] = others != 0 && page[k] >= 0 ? __ldcg(p.shares + page[k]) : kEvent;
 #pragma unroll
-        for (int k = 0; k < kHeld && first + 32 * k < e1; ++k) {
+        for (int k = 0; k < K && first + 32 * k < e1; ++k) {
             bool mine = page[k] >= 0;
             if (mine && shared) mine = settle(first + 32 * k + lane, page[k], word[k]);
             const unsigned votes = __ballot_sync(kFullMask, mine);
