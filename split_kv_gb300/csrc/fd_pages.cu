@@ -314,7 +314,11 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             page[k] = -2;
             if (first + 32 * k >= e1) break;
             if (e >= e1) continue;
-            if (b < 0 || e >= s_first[b + 1]) b = find(s_first, p.batch, e);
+            if (b < 0) b = find(s_first, p.batch, e);
+            for (int steps = 0; e >= s_first[b + 1]; ++steps) {     // most often the same sequence or one soon behind it
+                if (steps < 4) ++b;
+                else b = find(s_first, p.batch, e);
+            }
             const int j = ((s_keep[b] + ps1) >> p.page_shift) + e - s_first[b];
             page[k] = p.block_table[static_cast<int64_t>(b) * p.max_pages + j];
         }
@@ -327,14 +331,14 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
     };
     // calls f(first, pages) for the warp's references: the first kHeld of a thread at once,
     // whose pages stay in registers from phase to phase, others one by one
-    int held[kHeld];
+    int held[kHeld], words[kHeld];      // (and the pages' words, once every event has happened)
     auto for_references = [&](auto f) {
-        if (e0 < e1) f(e0, held);
+        if (e0 < e1) f(e0, held, words);
 #pragma unroll 1
         for (int first = e0 + 32 * kHeld; first < e1; first += 32) {
-            int page[1];
+            int page[1], word[1];
             load_pages(first, page);
-            f(first, page);
+            f(first, page, word);
         }
     };
     // calls f(b, page) for the thread's claims
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             if (left_of(was) < 0) raise(kStatusPageBit);      // let go more often than held
         };
         const int was0 = tail0 >= 0 ? atomicAdd(&p.shares[tail0], kEvent) : 0;
-        for_references([&](int first, auto& page) {
+        for_references([&](int first, auto& page, auto& word) {
             constexpr int K = sizeof(page) / sizeof(int);
             int was[K];
 #pragma unroll
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
         });
         for (int b = b0; b < p.batch; b += ranks * blockDim.x) bad_page |= s_keep[b] >= 0 && (s_keep[b] & ps1) != 0 && (b == b0 ? tail0 : tail_page(b)) < 0;
     } else {
-        for_references([&](int first, auto& page) {
+        for_references([&](int first, auto& page, auto& word) {
             constexpr int K = sizeof(page) / sizeof(int);
 #pragma unroll
             for (int k = 0; k < K && first + 32 * k < e1; ++k) given += page[k] >= 0;
@@ -395,28 +399,26 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
     if (others != 0) {
         cluster_barrier();              // (the counts are read before they are written again)
         auto bid = [&](int number, int page, int word) {
-            if (word != kEvent && (word <= -kCode || left_of(word) < 0)) atomicMin(&p.shares[page], code_of(number));
+            const bool bids = word != kEvent && (word <= -kCode || left_of(word) < 0);
+            if (bids) atomicMin(&p.shares[page], code_of(number));
+            return bids;
         };
-        auto words_of = [&](int first, auto& page, auto& word) {
+        for_references([&](int first, auto& page, auto& word) {
             constexpr int K = sizeof(page) / sizeof(int);
 #pragma unroll
             for (int k = 0; k < K && first + 32 * k < e1; ++k) word[k] = page[k] >= 0 ? __ldcg(p.shares + page[k]) : 0;
-        };
-        for_references([&](int first, auto& page) {
-            constexpr int K = sizeof(page) / sizeof(int);
-            int word[K];
-            words_of(first, page, word);
 #pragma unroll
             for (int k = 0; k < K && first + 32 * k < e1; ++k)
-                if (page[k] >= 0) bid(first + 32 * k + lane, page[k], word[k]);
+                if (page[k] >= 0 && bid(first + 32 * k + lane, page[k], word[k])) word[k] = -kCode;   // (to be read again)
         });
         for_claims([&](int b, int page) { bid(E + b, page, __ldcg(p.shares + page)); });
         cluster_barrier();
         given = 0;
-        for_references([&](int first, auto& page) {
+        for_references([&](int first, auto& page, auto& word) {
             constexpr int K = sizeof(page) / sizeof(int);
-            int word[K];
-            words_of(first, page, word);
+#pragma unroll
+            for (int k = 0; k < K && first + 32 * k < e1; ++k)
+                if (page[k] >= 0 && (K == 1 || word[k] == -kCode)) word[k] = __ldcg(p.shares + page[k]);
 #pragma unroll
             for (int k = 0; k < K && first + 32 * k < e1; ++k) given += page[k] >= 0 && (word[k] == kEvent || word[k] == code_of(first + 32 * k + lane));
         });
@@ -475,11 +477,13 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
             if (others != 0 && s_new[b] != kNone)
                 p.block_table[static_cast<int64_t>(b) * p.max_pages + (s_keep[b] >> p.page_shift)] = s_new[b];
         });
-    for_references([&](int first, auto& page) {
-            constexpr int K = sizeof(page) / sizeof(int);
-        int word[K];
+    for_references([&](int first, auto& page, auto& word) {
+        constexpr int K = sizeof(page) / sizeof(int);
 #pragma unroll
-        for (int k = 0; k < K && first + 32 * k < e1; ++k) word[k] = others != 0 && page[k] >= 0 ? __ldcg(p.shares + page[k]) : kEvent;
+        for (int k = 0; k < K && first + 32 * k < e1; ++k) {
+            if (others == 0) word[k] = kEvent;
+            else if (K == 1 && page[k] >= 0) word[k] = __ldcg(p.shares + page[k]);
+        }
 #pragma unroll
         for (int k = 0; k < K && first + 32 * k < e1; ++k) {
             bool mine = page[k] >= 0;
