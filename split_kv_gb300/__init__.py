@@ -275,11 +275,13 @@ def _check_scales(desc, scales: FdKvScales) -> None:
 
 
 _types = {}
+_int32 = None
 
 
 def _array(t, n: int, name: str, kind: str):
     """Address of n contiguous elements of the type, checked if t is a tensor (addresses and None go
-    unchecked, and so do a call's tensors that its descriptor was made from: 0.8 us each)."""
+    unchecked, and so do a call's tensors that its descriptor was made from: each check costs its time)."""
+    global _int32
     if t is None:
         return None
     try:
@@ -289,12 +291,19 @@ def _array(t, n: int, name: str, kind: str):
     if not _types:
         import torch
         _types.update(int32=torch.int32, int64=torch.int64, float32=torch.float32)
+        _int32 = torch.int32
     if dtype is not _types[kind] or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous {kind}")
     return t.data_ptr()
 
 
 def _i32(t, n: int, name: str):
+    """_array of int32, the short way."""
+    try:
+        if t.dtype is _int32 and t.numel() >= n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     return _array(t, n, name, "int32")
 
 
