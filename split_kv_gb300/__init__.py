@@ -7,6 +7,10 @@ marshalling only: torch tensors are passed as device pointers, streams as
 library's CUDA kernels.  There is no CPU fallback: if the library is missing
 the first call raises.
 
+A paged cache's life around the decode: fd_page_tables gives pages to new tokens, fd_qkv_rope and
+fd_cache_store fill them, fd_page_fork shares them, fd_page_trim gives them back, fd_page_compact and
+fd_page_copy move them.
+
 Typical use::
 
     import split_kv_gb300 as fd
