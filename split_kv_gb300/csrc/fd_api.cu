@@ -539,6 +539,7 @@ fd_status check_pool(const fd_pool& x, int32_t n_pages) {
     }
     if (x.page_stride < 1 || x.page_stride >= (int64_t(1) << 40)) return FD_ERR_INVALID_ARG;
     if (n_pages > 1 && x.page_stride < x.row_bytes) return FD_ERR_INVALID_ARG;
+    if (x.page_stride > (int64_t(1) << 46) / n_pages) return FD_ERR_INVALID_ARG;         // (offsets stay within 64 bits)
     return FD_OK;
 }
 

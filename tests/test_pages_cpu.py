@@ -182,7 +182,8 @@ def pool(fd, **over):
 
 
 @pytest.mark.parametrize("over", [
-    dict(base=None), dict(row_bytes=0), dict(row_bytes=-1), dict(reserved=1), dict(page_stride=0), dict(page_stride=-16), dict(page_stride=128),
+    dict(base=None), dict(row_bytes=0), dict(row_bytes=-1), dict(reserved=1), dict(page_stride=0), dict(page_stride=-16), dict(page_stride=128), dict(page_stride=1 << 39, stride=(0, 1 << 41)),
+    dict(page_stride=(1 << 46) // 9 + 1),
     dict(extent=(0, 0)), dict(extent=(1, -1)), dict(stride=(0, 0)), dict(stride=(1, 128)), dict(stride=(0, -4096)), dict(stride=(0, 1 << 41))])
 def test_copy_refuses_pools(fd, over):
     two = (fd.FdPool * 2)(pool(fd), pool(fd, **over))
