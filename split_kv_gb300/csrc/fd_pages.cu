@@ -511,7 +511,6 @@ __global__ void __launch_bounds__(1024) fd_page_trim_kernel(const PagePlanParams
 // (One map over all CTAs, marked and looked up remotely, was slower: 38 against 32 us
 // for 61000 held pages of a pool of 131072, half of it given up.)
 constexpr int kEntries = 16;            // entries of the free stack a thread holds in a round
-constexpr int kNothing = INT32_MAX;     // in the place of a page behind the last
 
 __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanParams p, int words_per_cta) {
     extern __shared__ int32_t s_mem[];
@@ -519,10 +518,9 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
     int32_t* s_pages = s_seg + p.batch + 1;                             // [batch] pages of the row
     const int words = words_per_cta * gridDim.x;
     uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_pages + p.batch);  // [words] this CTA's marks, then the joined map
-    uint32_t* s_pref = s_bits + words;                                  // [words] held pages of the range's words before
+    uint32_t* s_pref = s_bits + words;                                  // [words] held pages of the words before
     __shared__ long long s_sums[2][32];
     __shared__ uint32_t s_held[kMaxCtas], s_kept[2][kMaxCtas];          // of each CTA's range, and of its entries
-    __shared__ int32_t s_start[kMaxCtas];                               // held pages of the ranges before
     Scan scan{s_sums};
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x, ranks = gridDim.x;
     const int ps1 = (1 << p.page_shift) - 1, threads = blockDim.x;
@@ -567,43 +565,43 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
     cluster_wait();                 // every CTA has started
 
     const uint32_t bits = smem_u32(s_bits), pref = smem_u32(s_pref);
-    // A warp's segments of the rows: the pages of the first kCached of them stay in registers.
+    // A warp's segments of the rows; the first kCached of them stay in registers.
     constexpr int kPer = kSegment / 32, kCached = 2;
-    using Pages = int[kPer];
-    auto row_of = [&](int s, int& j0, int& n) {
+    struct Segment {
+        int32_t* row;               // the lane's first entry
+        int n;                      // entries from there on
+        int page[kPer];
+    };
+    auto load_segment = [&](int s, Segment& x) {
         const int b = find(s_seg, p.batch, s);
-        j0 = (s - s_seg[b]) * kSegment + lane;
-        n = s_pages[b];
-        return p.block_table + static_cast<int64_t>(b) * p.max_pages;
-    };
-    auto load_segment = [&](int s, Pages& page) {
-        int j0, n;
-        const int32_t* row = row_of(s, j0, n);
+        const int j0 = (s - s_seg[b]) * kSegment + lane;
+        x.n = s_pages[b] - j0;
+        x.row = p.block_table + static_cast<int64_t>(b) * p.max_pages + j0;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) page[k] = j0 + 32 * k < n ? min(row[j0 + 32 * k], INT32_MAX - 1) : kNothing;
+        for (int k = 0; k < kPer; ++k) x.page[k] = 32 * k < x.n ? x.row[32 * k] : 0;
     };
-    auto mark = [&](const Pages& page) {
+    bool bad_page = false;
+    auto moves = [&](const Segment& x, int k) { return 32 * k < x.n && x.page[k] >= p.n_keep && x.page[k] < p.n_pages; };
+    auto mark = [&](const Segment& x) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            if (page[k] < 0 || (page[k] >= p.n_pages && page[k] != kNothing)) {
-                raise(kStatusPageBit);
-            } else if (page[k] >= p.n_keep && page[k] != kNothing) {
-                const int x = page[k] - p.n_keep;
-                atomicOr(&s_bits[x >> 5], 1u << (x & 31));
-            }
+            bad_page |= 32 * k < x.n && (x.page[k] < 0 || x.page[k] >= p.n_pages);
+            const int bit = x.page[k] - p.n_keep;
+            if (moves(x, k)) atomicOr(&s_bits[bit >> 5], 1u << (bit & 31));
         }
     };
-    Pages cached[kCached];
+    Segment cached[kCached];
 #pragma unroll
     for (int c = 0; c < kCached; ++c)
         if (w0 + c * warps < segments) load_segment(w0 + c * warps, cached[c]);
 #pragma unroll
     for (int c = 0; c < kCached; ++c)
         if (w0 + c * warps < segments) mark(cached[c]);
+#pragma unroll 1
     for (int s = w0 + kCached * warps; s < segments; s += warps) {
-        Pages page;
-        load_segment(s, page);
-        mark(page);
+        Segment x;
+        load_segment(s, x);
+        mark(x);
     }
     // the entries of the free stack that stay in it or are used up
     const int count = free_entries(p, count_read);
@@ -614,9 +612,8 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
 #pragma unroll
         for (int k = 0; k < kEntries; ++k) {
             const int64_t i = base + static_cast<int64_t>(w0) * (32 * kEntries) + 32 * k + lane;
-            entry[k] = i < count ? min(entry[k], INT32_MAX - 1) : kNothing;
-            if (entry[k] < 0 || (entry[k] >= p.n_pages && entry[k] != kNothing)) raise(kStatusPageBit);
-            votes[k] = __ballot_sync(kFullMask, entry[k] >= 0 && entry[k] < p.n_keep);
+            bad_page |= i < count && (entry[k] < 0 || entry[k] >= p.n_pages);
+            votes[k] = __ballot_sync(kFullMask, i < count && entry[k] >= 0 && entry[k] < p.n_keep);
             n += __popc(votes[k]);
         }
         long long all;
@@ -663,6 +660,11 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
     int upto = low(scan(mine, cta_held)) - mine;
     if (tid < ranks) remote_store(remote_smem(smem_u32(&s_held[rank]), tid), static_cast<uint32_t>(low(cta_held)));
     cluster_barrier();              // the marks are read
+    int held = 0;
+    for (int r = 0; r < ranks; ++r) {
+        if (r < rank) upto += static_cast<int>(s_held[r]);
+        held += static_cast<int>(s_held[r]);
+    }
     for (int w = wa; w < wb; ++w) {
         const uint32_t word = s_pref[range + w];
         for (int r = 0; r < ranks; ++r) {
@@ -671,59 +673,52 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
         }
         upto += __popc(word);
     }
-    int held = 0;
-    for (int r = 0; r < ranks; ++r) {
-        if (tid == r) s_start[r] = held;
-        held += static_cast<int>(s_held[r]);
-    }
     cluster_barrier();              // the map, its numbers and the filtered stack are there for everyone
 
     const int moved = min(min(held, kept), p.n_copies);
-    auto rename = [&](int s, const Pages& page) {
-        int j0, n;
-        int32_t* row = row_of(s, j0, n);
+    auto rename = [&](const Segment& x) {
         int number[kPer], to[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
+            const int bit = x.page[k] - p.n_keep;
             number[k] = INT32_MAX;
-            if (page[k] < p.n_keep || page[k] >= p.n_pages || j0 + 32 * k >= n) continue;
-            const int x = page[k] - p.n_keep, w = x >> 5;
-            number[k] = s_start[w / words_per_cta] + static_cast<int>(s_pref[w]) + __popc(s_bits[w] & ((1u << (x & 31)) - 1u));
+            if (moves(x, k)) number[k] = static_cast<int>(s_pref[bit >> 5]) + __popc(s_bits[bit >> 5] & ((1u << (bit & 31)) - 1u));
         }
 #pragma unroll
         for (int k = 0; k < kPer; ++k) to[k] = number[k] < moved ? __ldcg(p.free_pages + kept - 1 - number[k]) : 0;
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
-            if (number[k] < moved) row[j0 + 32 * k] = to[k];
+            if (number[k] < moved) x.row[32 * k] = to[k];
     };
 #pragma unroll
     for (int c = 0; c < kCached; ++c)
-        if (w0 + c * warps < segments) rename(w0 + c * warps, cached[c]);
+        if (w0 + c * warps < segments) rename(cached[c]);
+#pragma unroll 1
     for (int s = w0 + kCached * warps; s < segments; s += warps) {
-        Pages page;
-        load_segment(s, page);
-        rename(s, page);
+        Segment x;
+        load_segment(s, x);
+        rename(x);
     }
-    // each CTA writes its range's part of the list and moves the counts, four pages a thread at a time
-    for (int x0 = tid; x0 < words_per_cta * 32; x0 += 4 * threads) {
-        int number[4], to[4], held_by[4];
+    // each CTA writes its range's part of the list and moves the counts, eight pages a thread at a time
+    for (int x0 = tid; x0 < words_per_cta * 32; x0 += 8 * threads) {
+        int number[8], to[8], held_by[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
             const int x = x0 + k * threads;
             number[k] = INT32_MAX;
             if (x >= words_per_cta * 32) continue;
             const uint32_t word = s_bits[range + (x >> 5)];
             if ((word >> lane) & 1u)
-                number[k] = s_start[rank] + static_cast<int>(s_pref[range + (x >> 5)]) + __popc(word & ((1u << lane) - 1u));
+                number[k] = static_cast<int>(s_pref[range + (x >> 5)]) + __popc(word & ((1u << lane) - 1u));
         }
         const int page0 = p.n_keep + range * 32 + x0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
             to[k] = number[k] < moved ? __ldcg(p.free_pages + kept - 1 - number[k]) : 0;
             held_by[k] = p.shares != nullptr && number[k] < moved ? p.shares[page0 + k * threads] : 0;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
             if (number[k] >= moved) continue;
             p.copy_src[number[k]] = page0 + k * threads;
             p.copy_dst[number[k]] = to[k];
@@ -738,6 +733,7 @@ __global__ void __launch_bounds__(512) fd_page_compact_kernel(const PagePlanPara
         *p.free_count_out = kept - moved;
         *p.copy_count = moved;
     }
+    if (bad_page) raise(kStatusPageBit);
 }
 
 // One cluster of `ctas` CTAs; more than 8 have to be allowed, once per context (large_ctx: the kernel's own).
@@ -803,7 +799,7 @@ cudaError_t launch_page_trim(const PagePlanParams& p, cudaStream_t stream) {
     // many as a cluster has, of 512.  Drafts of 64 sequences / 37600 references (pages of six
     // sequences among them, parts of which others keep), us with the copy that restores the
     // state (1.3): 8 x 128 7.0 / 75, 8 x 256 7.1 / 45, 8 x 512 7.3 / 33, 16 x 256 7.2 / 29, 16 x 512 7.5 / 19,
-    // 16 x 768 7.9 / 21; since a warp's loops end where its references do, 8 x 256 6.1, 16 x 512 19.
+    // 16 x 768 7.9 / 21; since then 8 x 256 5.6 to 6.1, 16 x 512 16.4.
     const bool small = static_cast<int64_t>(p.batch) * p.max_pages <= 16 * 8 * 256;
     return launch_cluster(fd_page_trim_kernel, large_ctx, small ? 8 : kMaxCtas, small ? 256 : 512, smem, stream, p);
 }
@@ -814,8 +810,9 @@ cudaError_t launch_page_compact(const PagePlanParams& p, cudaStream_t stream) {
     cudaError_t e = allow_smem(fd_page_compact_kernel, (2 * FD_MAX_TABLE_BATCH + 1 + 2 * kMaxWords) * sizeof(int32_t), configured_ctx);
     if (e != cudaSuccess) return e;
     // As many threads as hold tables and free stack in registers, within a cluster's.
-    // 32 sequences in a pool of 2048 / 61000 pages in one of 131072, us: 8 x 128 8.9 / 72, 8 x 256
-    // 9.2 / 42, 16 x 256 9.7 / 26, 16 x 512 10.5 / 19.
+    // 32 sequences in a pool of 2048 / 61000 pages in one of 131072, us with the copy that
+    // restores the state (1.2 / 1.7): 8 x 128 8.9 / 72, 8 x 256 9.2 / 42, 16 x 256 9.7 / 26, 16 x 512 10.5 / 19; since
+    // then 8 x 128 8.3, 16 x 512 17.4.
     const bool small = static_cast<int64_t>(p.batch) * p.max_pages <= 16384 && p.n_free_max <= 16384;
     const int ctas = small ? 8 : kMaxCtas;
     const int64_t words = (static_cast<int64_t>(p.n_pages) - p.n_keep + 31) / 32;
