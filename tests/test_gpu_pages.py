@@ -383,6 +383,25 @@ def test_compact_a_large_pool():
         same(run_compact(s, n_keep, s.n_pages), want, bad)
 
 
+def test_compact_as_large_as_it_gets():
+    """8192 sequences, and as many pages behind n_keep as a call takes."""
+    s = State(29, 8192, 8, 2, held=0.5, spare=fd.FD_MAX_COMPACT_PAGES)
+    n_keep = s.n_pages - fd.FD_MAX_COMPACT_PAGES
+    want, bad = want_compact(s, n_keep, 20000)
+    assert not bad and want["n"] > 1000
+    same(run_compact(s, n_keep, 20000), want)
+
+
+def test_forks_as_many_as_a_call_takes():
+    s = State(31, 8192, 8, 3, held=0.4, spare=9000)
+    children = [b for b, x in enumerate(s.lens) if x == 0]
+    parents = [int(x) for x in s.r.integers(0, 8192, size=8192)]
+    children = (children * 3)[:8192]                     # (most of them twice)
+    want, bad = want_fork(s, parents, children, None)
+    assert bad and want["n"] > 100
+    same(run_fork(s, parents, children, None), want, True)
+
+
 def test_compact_of_many_segments():
     s = State(23, 200, 16, 1100, held=1.0, spare=30000)
     for n_keep in (s.n_pages - s.count + 5000, s.n_pages - s.count):

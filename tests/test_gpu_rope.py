@@ -145,6 +145,31 @@ def test_weights(wtype, per_head):
     one(5, 90, 10, 5, "bf16", wtype=wtype, per_head=per_head)
 
 
+@pytest.mark.parametrize("rot,pairs", [(0, False), (16, True), (48, False), (64, True), (96, False), (112, True), (128, False)])
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+def test_rotated_part_of_many_rows(rot, pairs, cache):
+    """Enough rows for items of sixteen, the last of them in part."""
+    one(rot + 2, 900, 21, 5, "bf16", cache, rot=rot, pairs=pairs, k_rows=True, scale=0.9)
+
+
+@pytest.mark.parametrize("wtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("page", [0, 32])
+def test_weights_of_many_rows(wtype, per_head, page):
+    one(50, 1200, 18, 9, "f16", wtype=wtype, per_head=per_head, page=page)
+
+
+@pytest.mark.parametrize("n", [40, 1500, 9000])
+def test_heads_apart(n):
+    """Rows whose heads do not lie end to end, and ones whose tokens share a value row (a stride of 0)."""
+    s = Step(51, n, 12, 6, "bf16", "same")
+    x = torch.randn(n, 24, D, generator=gen(52), device=DEV).to(s.T)
+    s.q, s.k, s.v = x[:, ::2], x[:, 1:13:2], x[:1, :6].expand(n, 6, D)
+    want = s.want()
+    s.call()
+    s.check(want)
+
+
 def test_norm_without_weights_and_eps():
     one(6, 50, 4, 2, "f16", weights=False, eps=0.5)
     one(7, 50, 4, 2, "bf16", weights=False, eps=0.0)
