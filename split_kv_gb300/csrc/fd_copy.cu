@@ -1,7 +1,7 @@
 // fd_copy.cu -- pages copied within the pools of every layer (fd_page_copy).
 //
 // Bound by HBM: each byte is read once and written once.  Work is dealt in pieces
-// of a page of a pool; the list's length is read on the GPU.  Rows of 2 KB and
+// of a page of a pool; the list's length is read on the GPU.  Rows of 8 KB and
 // more of 16-byte units go by bulk copies through shared memory (500 pages of 32 KB in 64
 // pools, 2.1 GB: 320 us, 6.6 TB/s, 97 % of a plain copy's rate; by registers 330), all others
 // by registers.
@@ -25,7 +25,9 @@ constexpr int kAhead = 4;               // loads of a thread in flight
 // 6 stages, 3 loads, 2 CTAs 319.6 us; 12 / 8 / 1 324.6; 32 KB, 6 / 3 / 1 320.8; 8 KB, 6 / 3 / 4
 // 322.3, 24 / 12 / 1 540 (one thread issues too slowly); 4 KB, 12 / 6 / 4 333.
 constexpr int kPiece = 16384, kStages = 6, kAheadLoads = 3, kBulkCtas = 2;
-constexpr int kBulkRow = 2048;          // shorter rows by registers
+// Shorter rows by registers: a thread asks for one piece in about 0.3 us.  250 pages of 32 KB in 32
+// pools, as rows of 2 / 4 / 8 KB apart from each other, us: bulk 265 / 138 / 82, registers 87 / 86 / 86.
+constexpr int kBulkRow = 8192;
 
 // The first launch of a call waits for what came before it; a later one finds that ended.
 __device__ __forceinline__ void begin(bool first) {
@@ -33,32 +35,36 @@ __device__ __forceinline__ void begin(bool first) {
     grid_dependency_trigger();
 }
 
-// U: the unit that a thread moves.  A page is extent0 x extent1 rows of `per_row` units.
-template <typename U>
+// U: the unit that a thread moves.  A page is extent0 x extent1 rows of `per_row` units;
+// 2^TEAM threads take up to kAhead units each of it at a time.
+template <typename U, int TEAM>
 __global__ void __launch_bounds__(kCopyThreads) fd_page_copy_kernel(const CopyParams p, int64_t page_units, int chunks) {
     begin(p.first != 0);
     const int n = p.count != nullptr ? min(max(*p.count, 0), p.n_pairs) : p.n_pairs;
     const int64_t items = static_cast<int64_t>(n) * p.n_pools * chunks;
     const int64_t per_row = p.row_bytes / static_cast<int64_t>(sizeof(U));
     const bool flat = p.extent0 == 1 && p.extent1 == 1;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    constexpr int kTeams = kCopyThreads >> TEAM, kTeam = 1 << TEAM;
+    const int me = threadIdx.x & (kTeam - 1);
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * kTeams + (threadIdx.x >> TEAM); item < items;
+         item += static_cast<int64_t>(gridDim.x) * kTeams) {
         const int64_t pp = item / chunks;
         const int chunk = static_cast<int>(item - pp * chunks);
         const int pair = static_cast<int>(pp / p.n_pools), pool = static_cast<int>(pp - static_cast<int64_t>(pair) * p.n_pools);
         const int src = p.src[pair], dst = p.dst[pair];
         if (src < 0 || dst < 0 || src == dst) continue;
         if (src >= p.n_pages || dst >= p.n_pages) {
-            if (threadIdx.x == 0) atomicOr(&g_status, kStatusPageBit);
+            if (me == 0) atomicOr(&g_status, kStatusPageBit);
             continue;
         }
         const char* from = p.base[pool] + src * p.page_stride;
         char* to = p.base[pool] + dst * p.page_stride;
-        const int64_t u0 = static_cast<int64_t>(chunk) * (kCopyThreads * kAhead) + threadIdx.x;
+        const int64_t u0 = static_cast<int64_t>(chunk) * (kAhead * kTeam) + me;
         U v[kAhead];
         int64_t at[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int64_t u = u0 + k * kCopyThreads;
+            const int64_t u = u0 + k * kTeam;
             if (u >= page_units) continue;
             if (flat) {
                 at[k] = u * static_cast<int64_t>(sizeof(U));
@@ -71,7 +77,7 @@ __global__ void __launch_bounds__(kCopyThreads) fd_page_copy_kernel(const CopyPa
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (u0 + k * kCopyThreads < page_units) *reinterpret_cast<U*>(to + at[k]) = v[k];
+            if (u0 + k * kTeam < page_units) *reinterpret_cast<U*>(to + at[k]) = v[k];
     }
     if (p.first == 0) grid_dependency_wait();
 }
@@ -156,16 +162,26 @@ cudaError_t launch_copy_bulk(const CopyParams& p, cudaStream_t stream) {
                       p, static_cast<int>(pieces));
 }
 
-template <typename U>
-cudaError_t launch_copy_u(const CopyParams& p, cudaStream_t stream) {
-    const int64_t units = static_cast<int64_t>(p.extent0) * p.extent1 * (p.row_bytes / static_cast<int64_t>(sizeof(U)));
-    const int64_t chunks = (units + kCopyThreads * kAhead - 1) / (kCopyThreads * kAhead);
+template <typename U, int TEAM>
+cudaError_t launch_copy_team(const CopyParams& p, int64_t units, cudaStream_t stream) {
+    constexpr int64_t kTeams = kCopyThreads >> TEAM, kChunk = kAhead << TEAM;
+    const int64_t chunks = (units + kChunk - 1) / kChunk;
     if (chunks > INT32_MAX) return cudaErrorInvalidValue;
     const int sms = fd_num_sms(-1);
     if (sms < 1) return cudaErrorInvalidDevice;
-    const int64_t items = chunks * p.n_pools * p.n_pairs, most = static_cast<int64_t>(sms) * 8;
-    return launch_pdl(fd_page_copy_kernel<U>, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(kCopyThreads), 0,
+    const int64_t ctas = (chunks * p.n_pools * p.n_pairs + kTeams - 1) / kTeams, most = static_cast<int64_t>(sms) * 8;
+    return launch_pdl(fd_page_copy_kernel<U, TEAM>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(kCopyThreads), 0,
                       stream, p, units, static_cast<int>(chunks));
+}
+
+template <typename U>
+cudaError_t launch_copy_u(const CopyParams& p, cudaStream_t stream) {
+    // A page gets as many threads, whole warps, as it has kAhead units for.  8.2 MB of pages
+    // of 1 / 2 / 4 KB in each of 32 pools, us: 430 / 219 / 130 with 256 threads a page, 90 / 86 / 84 so.
+    const int64_t units = static_cast<int64_t>(p.extent0) * p.extent1 * (p.row_bytes / static_cast<int64_t>(sizeof(U)));
+    if (units <= kAhead << 5) return launch_copy_team<U, 5>(p, units, stream);
+    if (units <= kAhead << 6) return launch_copy_team<U, 6>(p, units, stream);
+    return launch_copy_team<U, 8>(p, units, stream);
 }
 
 }  // namespace
