@@ -35,7 +35,8 @@ constexpr unsigned kFullMask = 0xffffffffu;
 // of rows on their way.  16384 tokens, 32 / 8 heads, bf16, into a cache (403 MB): 68.7 us, 5.9
 // TB/s.  By the way there: 12 warps an SM with 4 stages 76 against 71.5, 20 with 8-row
 // stages 120 (spills); all rows through registers instead, 2 / 3 / 4 groups
-// ahead, 96 / 105 / 125; two groups' sums and roots side by side, no change.
+// ahead, 96 / 105 / 125; two groups' sums and roots side by side, no change; keys and
+// values of eight heads as one item, 70.4 against 69 (8 / 1 heads, 60000 tokens: 100 against 109).
 constexpr int kRopeWarps = 4;
 constexpr int kRopeCtas = 4;            // per SM
 constexpr int kRopeStages = 3;          // items of rows that a warp has in flight
