@@ -41,14 +41,17 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
     return w;
 }
 
+__device__ __forceinline__ float nan_for_inf(float x) {
+    return fabsf(x) <= 3.402823466e38f ? x : __uint_as_float(0x7fc00000u);
+}
+
 // two values to E4M3, nearest even; NaN stays NaN, and with SPECIAL infinities
 // become NaN (the conversion would make them 448)
 template <bool SPECIAL>
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
     if constexpr (SPECIAL) {
-        const float nan = __uint_as_float(0x7fc00000u);
-        a = fabsf(a) <= 3.402823466e38f ? a : nan;
-        b = fabsf(b) <= 3.402823466e38f ? b : nan;
+        a = nan_for_inf(a);
+        b = nan_for_inf(b);
     }
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }

@@ -88,12 +88,13 @@ __device__ __forceinline__ uint4 pack8(const float2* x) {
     return make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y), pack2<T>(x[2].x, x[2].y), pack2<T>(x[3].x, x[3].y));
 }
 
+// A product that overflows is of a finite value: 448, as the conversion makes it.
+__device__ __forceinline__ uint32_t quantised2(float2 x, float inv) {
+    return to_e4m3x2<false>(nan_for_inf(x.x) * inv, nan_for_inf(x.y) * inv);
+}
+
 __device__ __forceinline__ uint2 quantised8(const float2* x, float inv) {
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        w[h] = to_e4m3x2<true>(x[2 * h].x * inv, x[2 * h].y * inv) | (to_e4m3x2<true>(x[2 * h + 1].x * inv, x[2 * h + 1].y * inv) << 16);
-    return make_uint2(w[0], w[1]);
+    return make_uint2(quantised2(x[0], inv) | (quantised2(x[1], inv) << 16), quantised2(x[2], inv) | (quantised2(x[3], inv) << 16));
 }
 
 // An item is up to 4 GROUPS rows of one token: of its queries, its keys or its

@@ -1,5 +1,7 @@
 """fd_qkv_rope on the GPU against 64 bits (pages_ref.rope: the tolerance of 32-bit
 arithmetic is derived there; each output adds half a step of its type)."""
+import math
+
 import pytest
 import torch
 
@@ -327,3 +329,25 @@ def test_same_bits_whatever_the_batch():
         d = fd.make_rope_desc(s.q[a:b], s.k[a:b], q_out=q, k_out=k, q_weight=s.qw, k_weight=s.kw)
         fd.check(fd.fd_qkv_rope(d, s.q[a:b], s.k[a:b], None, s.qw, s.kw, s.freq, s.pos[a:b].contiguous(), None, q, k, None, None))
         assert torch.equal(q, s.q_out[a:b]) and torch.equal(k, s.k_out[a:b])
+
+
+@pytest.mark.parametrize("n", [40, 900])
+@pytest.mark.parametrize("scale", [1 / 64, 2.0 ** -126])
+def test_e4m3_of_large_finite_values(n, scale):
+    """A finite value whose quotient by the scale overflows 32 bits is beyond 448 like any other: 448, not NaN.
+    Infinities and NaN stay NaN."""
+    s = Step(21, n, 4, 4, "bf16", "e4m3", norm=False, rot=64)
+    s.ks = s.vs = scale
+    s.v[6, 3, :4] = torch.tensor([1e37, -3.3e38, float("inf"), float("nan")], device=DEV)
+    s.k[7, 2, 64:68] = torch.tensor([3.3e38, -1e37, float("-inf"), float("nan")], device=DEV)   # (of the part that is not rotated)
+    s.k[8, 1, 3], s.pos[8] = 1e37, 3                                                           # of a rotated pair
+    s.call()
+    tok = s.kc.shape[2]
+    rows = lambda cache, t, h: cache[s.slots[t] // tok, h, s.slots[t] % tok].float()
+    v, k, turned = rows(s.vc, 6, 3)[:4], rows(s.kc, 7, 2)[64:68], rows(s.kc, 8, 1)
+    assert v[:2].tolist() == [448.0, -448.0] and bool(torch.isnan(v[2:]).all())
+    assert k[:2].tolist() == [448.0, -448.0] and bool(torch.isnan(k[2:]).all())
+    a = 3 * float(s.freq[3])
+    want = [math.copysign(448.0, math.cos(a)), math.copysign(448.0, math.sin(a))]
+    assert [float(turned[3]), float(turned[3 + 32])] == want
+    assert int(torch.isnan(s.kc.float()).sum()) == 2 and int(torch.isnan(s.vc.float()).sum()) == 2
