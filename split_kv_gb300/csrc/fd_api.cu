@@ -519,6 +519,14 @@ PoolShape pool_shape(const fd_pool& x) {
     return s;
 }
 
+bool same_shape(const fd_pool& a, const fd_pool& b) {
+    if (a.page_stride != b.page_stride) return false;
+    if (a.stride[0] == b.stride[0] && a.stride[1] == b.stride[1] &&
+        a.extent[0] == b.extent[0] && a.extent[1] == b.extent[1] && a.row_bytes == b.row_bytes)
+        return true;
+    return pool_shape(a) == pool_shape(b);
+}
+
 int pool_unit(const PoolShape& s, const void* base) {
     const uint64_t bits = static_cast<uint64_t>(s.page_stride) | static_cast<uint64_t>(s.stride0) |
                           static_cast<uint64_t>(s.stride1) | static_cast<uint64_t>(s.row_bytes) |
@@ -958,33 +966,37 @@ fd_status fd_page_copy(const fd_pool* pools, int32_t n_pools, int32_t n_pages, i
     if (!ints_ok({}, {copy_src, copy_dst, copy_count})) return FD_ERR_INVALID_ARG;
     if (n_pools == 0 || n_pairs == 0) return FD_OK;   // (an empty tensor's address is null)
     if (copy_src == nullptr || copy_dst == nullptr) return FD_ERR_INVALID_ARG;
-    // one launch for the pools of one shape that follow each other
-    int first = 0;
-    while (first < n_pools) {
-        const PoolShape s = pool_shape(pools[first]);
-        fdk::CopyParams p = {};
-        p.page_stride = s.page_stride;
-        p.stride0 = s.stride0;
-        p.stride1 = s.stride1;
-        p.extent0 = static_cast<int32_t>(s.extent0);
-        p.extent1 = static_cast<int32_t>(s.extent1);
-        p.row_bytes = s.row_bytes;
-        p.unit = 16;
-        int n = 0;
-        for (; n < fdk::kPoolsPerLaunch && first + n < n_pools; ++n) {
-            if (n > 0 && !(pool_shape(pools[first + n]) == s)) break;
-            p.base[n] = static_cast<char*>(pools[first + n].base);
-            p.unit = std::min(p.unit, pool_unit(s, p.base[n]));
+    // One launch for (up to kPoolsPerLaunch) pools of one shape, wherever they are among kPoolsAtOnce:
+    // a launch waits for the one before it, and no two pools share memory.
+    constexpr int kPoolsAtOnce = 1024;
+    for (int base = 0; base < n_pools; base += kPoolsAtOnce) {
+        const int end = std::min(n_pools - base, kPoolsAtOnce);
+        const fd_pool* at = pools + base;
+        bool taken[kPoolsAtOnce] = {};
+        for (int first = 0; first < end; ++first) {
+            if (taken[first]) continue;
+            const PoolShape s = pool_shape(at[first]);
+            fdk::CopyParams p = {};
+            p.page_stride = s.page_stride;
+            p.stride0 = s.stride0;
+            p.stride1 = s.stride1;
+            p.extent0 = static_cast<int32_t>(s.extent0);
+            p.extent1 = static_cast<int32_t>(s.extent1);
+            p.row_bytes = s.row_bytes;
+            p.unit = 16;
+            for (int i = first; i < end && p.n_pools < fdk::kPoolsPerLaunch; ++i) {
+                if (taken[i] || !same_shape(at[i], at[first])) continue;
+                taken[i] = true;
+                p.base[p.n_pools++] = static_cast<char*>(at[i].base);
+                p.unit = std::min(p.unit, pool_unit(s, at[i].base));
+            }
+            p.n_pages = n_pages;
+            p.n_pairs = n_pairs;
+            p.src = copy_src;
+            p.dst = copy_dst;
+            p.count = copy_count;
+            if (fdk::launch_page_copy(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FD_ERR_CUDA;
         }
-        p.n_pools = n;
-        p.n_pages = n_pages;
-        p.n_pairs = n_pairs;
-        p.first = first == 0;
-        p.src = copy_src;
-        p.dst = copy_dst;
-        p.count = copy_count;
-        if (fdk::launch_page_copy(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FD_ERR_CUDA;
-        first += n;
     }
     return FD_OK;
 }

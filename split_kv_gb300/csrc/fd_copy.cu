@@ -6,9 +6,10 @@
 // pools, 2.1 GB: 320 us, 6.6 TB/s, 97 % of a plain copy's rate; by registers 330), all others
 // by registers.
 //
-// Pools of several shapes are a launch each.  The later ones do not wait for the one
-// before them: each launch lets the next one start only when what came before
-// the first has ended, and ends itself only after the one before it.
+// Pools of several shapes are a launch each, and every launch waits for the one before
+// it before its first read: what wrote the list and the pages is visible to a grid
+// only by a wait of its own, so none may rely on that of the call's first launch.
+// (12 pages of 64 KB in 32 pools and the scales of 32 more: 12.6 us; 10.8 without that wait.)
 #include "../../include/fd.h"
 #include "fd_device.cuh"
 #include "fd_internal.h"
@@ -29,17 +30,12 @@ constexpr int kPiece = 16384, kStages = 6, kAheadLoads = 3, kBulkCtas = 2;
 // pools, as rows of 2 / 4 / 8 KB apart from each other, us: bulk 265 / 138 / 82, registers 87 / 86 / 86.
 constexpr int kBulkRow = 8192;
 
-// The first launch of a call waits for what came before it; a later one finds that ended.
-__device__ __forceinline__ void begin(bool first) {
-    if (first) grid_dependency_wait();
-    grid_dependency_trigger();
-}
-
 // U: the unit that a thread moves.  A page is extent0 x extent1 rows of `per_row` units;
 // 2^TEAM threads take up to kAhead units each of it at a time.
 template <typename U, int TEAM>
 __global__ void __launch_bounds__(kCopyThreads) fd_page_copy_kernel(const CopyParams p, int64_t page_units, int chunks) {
-    begin(p.first != 0);
+    grid_dependency_trigger();
+    grid_dependency_wait();
     const int n = p.count != nullptr ? min(max(*p.count, 0), p.n_pairs) : p.n_pairs;
     const int64_t items = static_cast<int64_t>(n) * p.n_pools * chunks;
     const int64_t per_row = p.row_bytes / static_cast<int64_t>(sizeof(U));
@@ -79,7 +75,6 @@ __global__ void __launch_bounds__(kCopyThreads) fd_page_copy_kernel(const CopyPa
         for (int k = 0; k < kAhead; ++k)
             if (u0 + k * kTeam < page_units) *reinterpret_cast<U*>(to + at[k]) = v[k];
     }
-    if (p.first == 0) grid_dependency_wait();
 }
 
 // One thread a CTA asks for pieces of up to kPiece bytes of a row and sends them
@@ -91,7 +86,8 @@ __global__ void __launch_bounds__(32) fd_page_bulk_kernel(const __grid_constant_
     if (threadIdx.x != 0) return;
     for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
     fence_barrier_init();
-    begin(p.first != 0);
+    grid_dependency_trigger();
+    grid_dependency_wait();
     const int n = p.count != nullptr ? min(max(*p.count, 0), p.n_pairs) : p.n_pairs;
     const int64_t per_page = static_cast<int64_t>(p.extent0) * p.extent1 * pieces;
     const int64_t items = static_cast<int64_t>(n) * p.n_pools * per_page;
@@ -146,7 +142,6 @@ __global__ void __launch_bounds__(32) fd_page_bulk_kernel(const __grid_constant_
     }
     if (late) atomicOr(&g_status, kStatusTimeoutBit);
     bulk_wait<0>();
-    if (p.first == 0) grid_dependency_wait();
 }
 
 cudaError_t launch_copy_bulk(const CopyParams& p, cudaStream_t stream) {

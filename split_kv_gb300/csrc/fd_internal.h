@@ -261,7 +261,6 @@ struct CopyParams {                 // pools of one geometry; bytes
     int32_t extent0, extent1;
     int32_t unit;                   // bytes that divide addresses, strides and row_bytes: 1, 2, 4, 8 or 16
     int32_t n_pools, n_pages, n_pairs;
-    int32_t first;                  // of the call's launches
     const int32_t* src;
     const int32_t* dst;
     const int32_t* count;           // or null

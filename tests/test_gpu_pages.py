@@ -633,3 +633,103 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for x, w in zip(t, want):
         same(x, w)
+
+
+# ------------------------------------------------------------------ copies of several shapes, behind what writes their list
+def mixed_pools(P, layers, seed=200):
+    """Keys, values and the scales of both, layer after layer, with a pool of odd rows here and there."""
+    out = []
+    for k in range(layers):
+        out += [rand_bytes(seed + 5 * k, torch.float8_e4m3fn, P, 4, 32, 128), rand_bytes(seed + 5 * k + 1, torch.float8_e4m3fn, P, 4, 32, 128),
+                rand_bytes(seed + 5 * k + 2, torch.float32, P, 4, 2), rand_bytes(seed + 5 * k + 3, torch.float32, P, 4, 2)]
+        if k % 5 == 0:
+            out.append(rand_bytes(seed + 5 * k + 4, torch.uint8, P, 3, 7))
+    return out
+
+
+@pytest.mark.parametrize("layers", [1, 6, 36])
+def test_copy_of_pools_in_any_order(layers):
+    """One launch takes the pools of a shape wherever they are in the list (36 layers: more than a launch takes)."""
+    P = 20
+    pools = mixed_pools(P, layers)
+    perm = [int(x) for x in np.random.default_rng(layers).permutation(P)]
+    src, dst = perm[:9], perm[9:18]
+    src[3], dst[5] = -1, -1
+    want = [copied(x, zip(src, dst)) for x in pools]
+    fd.check(fd.fd_page_copy(fd.make_pools(pools), i32(src), i32(dst)))
+    for x, y in zip(pools, want):
+        assert torch.equal(bits(x), bits(y))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_copies_of_several_shapes_behind_forks_and_trims(captured):
+    """Lists that a fork and a trim write directly ahead of the copies, over and over: every launch of a
+    copy sees the list of the call before it, not that of the round before, and its pages."""
+    states = []
+    for seed in range(2):
+        s = State(90 + seed, 40, 16, 12, held=0.6, spare=200, empty=12)
+        s.n_pages = 480
+        perm = [int(x) for x in s.r.permutation(480)]
+        have = [-(-x // 16) for x in s.lens]
+        at = np.concatenate([[0], np.cumsum(have)])
+        s.table = [perm[at[b]:at[b + 1]] + [-9] * (12 - have[b]) for b in range(40)]
+        s.free = perm[at[-1]:]
+        s.count = len(s.free)
+        s.free += [-5] * (480 - s.count)
+        s.shares = [0] * 480
+        parents, children, keep = s.forked(8)
+        start = dict(lens=s.lens, count=[s.count], table=s.table, free=s.free, shares=s.shares, parents=parents, children=children, keep=keep)
+        forked, bad = want_fork(s, parents, children, keep)
+        assert not bad and forked["n"] > 2
+        s.take(forked)
+        cut = random_keep(s, s.r)
+        trimmed, bad = want_trim(s, cut)
+        assert not bad and trimmed["n"] > 0
+        pairs = [list(zip(o["src"], o["dst"]))[:o["n"]] for o in (forked, trimmed)]
+        states.append(({k: i32(v) for k, v in dict(start, cut=cut).items()}, pairs, trimmed))
+    pools = mixed_pools(480, 3)
+    first = [x.clone() for x in pools]
+    want = []
+    for _, pairs, _ in states:
+        y = first
+        for p in pairs:
+            y = [copied(x, p) for x in y]
+        want.append(y)
+    handle = fd.make_pools(pools)
+    now = {k: v.clone() for k, v in states[0][0].items()}
+    given = {k: v.clone() for k, v in now.items()}
+    table = now["table"].view(40, 12)
+    src, dst, n, lens2, count2 = i32([-1] * 40), i32([-1] * 40), i32([0]), torch.zeros_like(now["lens"]), i32([0])
+    desc = fd.make_page_desc(table, now["free"], None, copies=src, page_size=16, n_pages=480)
+
+    def step():
+        for x, y in zip(pools, first):
+            bits(x).copy_(bits(y))
+        for k in now:
+            now[k].copy_(given[k])
+        src.fill_(-1), dst.fill_(-1), n.zero_()
+        fd.check(fd.fd_page_fork(desc, now["parents"], now["children"], now["keep"], now["lens"], now["free"], now["count"], table,
+                                 now["shares"], lens2, count2, src, dst, n))
+        fd.check(fd.fd_page_copy(handle, src, dst, n))
+        fd.check(fd.fd_page_trim(desc, now["cut"], lens2, now["free"], count2, table, now["shares"], lens2, count2, src, dst, n))
+        fd.check(fd.fd_page_copy(handle, src, dst, n))
+
+    step()
+    torch.cuda.synchronize()
+    run = step
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        run = graph.replay
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for k in range(60):
+        values, _, out = states[k % 2]
+        for name in given:
+            given[name].copy_(values[name])
+        run()
+        for x, y in zip(pools, want[k % 2]):
+            wrong += (bits(x) != bits(y)).sum()
+        wrong += (lens2 != i32(out["lens"])).sum() + (table != i32(out["table"])).sum()
+    assert int(wrong) == 0
+    assert fd.fd_device_status(clear=True) == fd.FD_OK
