@@ -109,6 +109,7 @@ class FdPageDesc(ctypes.Structure):
     """Mirror of ``fd_page_desc`` (include/fd.h)."""
     _fields_ = [(n, ctypes.c_int32) for n in ("batch", "page_size", "max_pages_per_seq", "n_pages",
                                               "n_free_max", "n_slots")]
+    copy_list = False       # make_page_desc: n_slots counts a copy list, not a slot map
 
 
 class FdPromptDesc(ctypes.Structure):
@@ -303,6 +304,8 @@ def _array(t, n: int, name: str, kind: str):
 
 def _i32(t, n: int, name: str):
     """_array of int32, the short way."""
+    if t is None:
+        return None
     try:
         if t.dtype is _int32 and t.numel() >= n and t.is_contiguous():
             return t.data_ptr()
@@ -431,10 +434,14 @@ def fd_cache_store(desc: FdStoreDesc, scales: FdKvScales, k, v, slots, k_cache, 
 def fd_page_tables(desc: FdPageDesc, seqlens, new_tokens, free_pages, free_count, block_table, seqlens_out,
                    free_count_out, cu_tokens, slots, positions, stream=None) -> int:
     """Pages for the new tokens of a step, and each new token's slot and position."""
-    return int(_load().fd_page_tables(ctypes.byref(desc), _ptr(seqlens), _ptr(new_tokens), _ptr(free_pages),
-                                      _ptr(free_count), _ptr(block_table), _ptr(seqlens_out),
-                                      _ptr(free_count_out), _ptr(cu_tokens), _ptr(slots), _ptr(positions),
-                                      _stream(stream)))
+    if desc.copy_list:
+        raise ValueError("fd_page_tables takes a descriptor of a slot map, this one is of a copy list")
+    b, n = desc.batch, desc.n_slots
+    return _load().fd_page_tables(ctypes.byref(desc), _i32(seqlens, b, "seqlens"), _i32(new_tokens, b, "new_tokens"),
+                                  _i32(free_pages, desc.n_free_max, "free_pages"), _i32(free_count, 1, "free_count"),
+                                  _i32(block_table, b * desc.max_pages_per_seq, "block_table"), _i32(seqlens_out, b, "seqlens_out"),
+                                  _i32(free_count_out, 1, "free_count_out"), _i32(cu_tokens, b + 1, "cu_tokens"),
+                                  _array(slots, n, "slots", "int64"), _i32(positions, n, "positions"), _stream(stream))
 
 
 def fd_prompt_workspace_size(desc: FdPromptDesc) -> int:
@@ -630,6 +637,7 @@ def make_page_desc(block_table, free_pages, slots, *, page_size: int, n_pages: i
     d.page_size, d.n_pages = int(page_size), int(n_pages)
     d.n_free_max = free_pages.numel()
     d.n_slots = slots.numel() if slots is not None else copies.numel() if copies is not None else 0
+    d.copy_list = slots is None
     return d
 
 

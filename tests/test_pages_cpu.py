@@ -236,3 +236,34 @@ def test_reference_compact_by_hand():
     # F = 0, 2; 5 -> 2, 6 -> 0
     assert not bad and out["table"] == [[0, 1], [0, 2]] and out["count"] == 0 and out["n"] == 2
     assert out["src"][:2] == [5, 6] and out["dst"][:2] == [2, 0] and out["shares"][0] == 1 and out["shares"][6] == 0
+
+
+# ------------------------------------------------------------------ fd_page_tables
+def tables_args():
+    i = lambda n: torch.zeros(n, dtype=torch.int32)
+    return dict(seqlens=i(3), new_tokens=i(3), free_pages=i(9), free_count=i(1), block_table=i(24).view(3, 8), seqlens_out=i(3),
+                free_count_out=i(1), cu_tokens=i(4), slots=torch.zeros(6, dtype=torch.int64), positions=i(6), stream=0)
+
+
+def test_tables_refuse_a_copy_lists_descriptor(fd):
+    """Its n_slots is the list's length: slots and positions may be shorter, and would be written behind their ends."""
+    a = tables_args()
+    for copies in (torch.zeros(100, dtype=torch.int32), torch.zeros(6, dtype=torch.int32), None):
+        d = fd.make_page_desc(a["block_table"], a["free_pages"], None, copies=copies, page_size=16, n_pages=9)
+        with pytest.raises(ValueError):
+            fd.fd_page_tables(d, **a)
+
+
+def test_tables_binding_refuses_sizes(fd):
+    i = lambda n: torch.zeros(n, dtype=torch.int32)
+    a = tables_args()
+    d = fd.make_page_desc(a["block_table"], a["free_pages"], a["slots"], page_size=16, n_pages=9)
+    for n, v in (("seqlens", i(2)), ("seqlens", i(3).long()), ("new_tokens", i(2)), ("new_tokens", i(6)[::2]), ("free_pages", i(8)), ("free_count", i(0)),
+                 ("free_count", i(1).long()), ("block_table", i(23)), ("block_table", i(48).view(3, 16)[:, ::2]), ("seqlens_out", i(2)), ("free_count_out", i(0)),
+                 ("cu_tokens", i(3)), ("slots", torch.zeros(5, dtype=torch.int64)), ("slots", i(6)), ("positions", i(5)),
+                 ("positions", torch.zeros(6, dtype=torch.int64))):
+        with pytest.raises(ValueError):
+            fd.fd_page_tables(d, **{**a, n: v})
+    d.page_size = 4         # (whatever the sizes: refused by the library, so that nothing reaches a GPU here)
+    assert fd.fd_page_tables(d, **a) == fd.FD_ERR_UNSUPPORTED
+    assert fd.fd_page_tables(d, **{**a, "cu_tokens": None, "positions": None}) == fd.FD_ERR_UNSUPPORTED
