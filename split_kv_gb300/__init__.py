@@ -285,7 +285,7 @@ _int32 = None
 
 def _array(t, n: int, name: str, kind: str):
     """Address of n contiguous elements of the type, checked if t is a tensor (addresses and None go
-    unchecked, and so do a call's tensors that its descriptor was made from: each check costs its time)."""
+    unchecked)."""
     global _int32
     if t is None:
         return None
@@ -466,46 +466,50 @@ def fd_qkv_rope(desc: FdRopeDesc, q, k, v, q_weight, k_weight, inv_freq, positio
                                _array(slots, n, "slots", "int64"), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _stream(stream))
 
 
+def _page_arrays(desc, free_pages, free_count, block_table, shares, free_count_out, copy_src, copy_dst, copy_count):
+    """Addresses of what fd_page_fork, _trim and _compact take alike, as large as their descriptor says."""
+    n = desc.n_slots
+    return (_i32(free_pages, desc.n_free_max, "free_pages"), _i32(free_count, 1, "free_count"),
+            _i32(block_table, desc.batch * desc.max_pages_per_seq, "block_table"), _i32(shares, desc.n_pages, "shares"),
+            _i32(free_count_out, 1, "free_count_out"), _i32(copy_src, n, "copy_src"), _i32(copy_dst, n, "copy_dst"),
+            _i32(copy_count, 1, "copy_count"))
+
+
 def fd_page_fork(desc: FdPageDesc, parents, children, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out,
                  free_count_out, copy_src, copy_dst, copy_count, n_forks: int | None = None, stream=None) -> int:
     """Sequences children[i] that share the pages of parents[i]'s first keep[i] tokens (None: of all)."""
     n = parents.numel() if n_forks is None else int(n_forks)
     b = desc.batch
-    return _load().fd_page_fork(ctypes.byref(desc), n, _i32(parents, n, "parents"), _i32(children, n, "children"),
-                                _i32(keep, n, "keep"), _i32(seqlens, b, "seqlens"), _ptr(free_pages),
-                                _ptr(free_count), _ptr(block_table),
-                                _i32(shares, desc.n_pages, "shares"), _i32(seqlens_out, b, "seqlens_out"), _ptr(free_count_out),
-                                _ptr(copy_src), _i32(copy_dst, desc.n_slots, "copy_dst"), _ptr(copy_count),
-                                _stream(stream))
+    free, count, table, held, count_out, src, dst, copies = _page_arrays(desc, free_pages, free_count, block_table, shares, free_count_out,
+                                                                         copy_src, copy_dst, copy_count)
+    return _load().fd_page_fork(ctypes.byref(desc), n, _i32(parents, n, "parents"), _i32(children, n, "children"), _i32(keep, n, "keep"),
+                                _i32(seqlens, b, "seqlens"), free, count, table, held, _i32(seqlens_out, b, "seqlens_out"), count_out, src,
+                                dst, copies, _stream(stream))
 
 
 def fd_page_trim(desc: FdPageDesc, keep, seqlens, free_pages, free_count, block_table, shares, seqlens_out, free_count_out,
                  copy_src=None, copy_dst=None, copy_count=None, stream=None) -> int:
     """Sequences cut to their first keep[b] tokens; pages that nobody holds any more go back to the free stack."""
     b = desc.batch
-    return _load().fd_page_trim(ctypes.byref(desc), _i32(keep, b, "keep"), _i32(seqlens, b, "seqlens"),
-                                _ptr(free_pages), _ptr(free_count),
-                                _ptr(block_table), _i32(shares, desc.n_pages, "shares"),
-                                _i32(seqlens_out, b, "seqlens_out"), _ptr(free_count_out), _ptr(copy_src),
-                                _i32(copy_dst, desc.n_slots, "copy_dst"), _ptr(copy_count), _stream(stream))
+    free, count, table, held, count_out, src, dst, copies = _page_arrays(desc, free_pages, free_count, block_table, shares, free_count_out,
+                                                                         copy_src, copy_dst, copy_count)
+    return _load().fd_page_trim(ctypes.byref(desc), _i32(keep, b, "keep"), _i32(seqlens, b, "seqlens"), free, count, table, held,
+                                _i32(seqlens_out, b, "seqlens_out"), count_out, src, dst, copies, _stream(stream))
 
 
 def fd_page_compact(desc: FdPageDesc, n_keep: int, seqlens, free_pages, free_count, block_table, shares, free_count_out,
                     copy_src, copy_dst, copy_count, stream=None) -> int:
     """Held pages from n_keep on renamed to free pages below it, for the high end of a pool to be given up."""
-    b = desc.batch
-    return _load().fd_page_compact(ctypes.byref(desc), int(n_keep), _i32(seqlens, b, "seqlens"),
-                                   _ptr(free_pages), _ptr(free_count),
-                                   _ptr(block_table), _i32(shares, desc.n_pages, "shares"),
-                                   _ptr(free_count_out), _ptr(copy_src), _i32(copy_dst, desc.n_slots, "copy_dst"),
-                                   _ptr(copy_count), _stream(stream))
+    return _load().fd_page_compact(ctypes.byref(desc), int(n_keep), _i32(seqlens, desc.batch, "seqlens"),
+                                   *_page_arrays(desc, free_pages, free_count, block_table, shares, free_count_out, copy_src, copy_dst,
+                                                 copy_count), _stream(stream))
 
 
 def fd_page_copy(pools, copy_src, copy_dst, copy_count=None, n_pairs: int | None = None, stream=None) -> int:
     """Page copy_dst[i] of every pool (make_pools) becomes what page copy_src[i] is."""
     n = copy_src.numel() if n_pairs is None else int(n_pairs)
     return _load().fd_page_copy(pools, len(pools), pools.n_pages, n, _i32(copy_src, n, "copy_src"), _i32(copy_dst, n, "copy_dst"),
-                                _ptr(copy_count), _stream(stream))
+                                _i32(copy_count, 1, "copy_count"), _stream(stream))
 
 
 def fd_device_status(stream=None, clear: bool = True) -> int:

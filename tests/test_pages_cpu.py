@@ -267,3 +267,37 @@ def test_tables_binding_refuses_sizes(fd):
     d.page_size = 4         # (whatever the sizes: refused by the library, so that nothing reaches a GPU here)
     assert fd.fd_page_tables(d, **a) == fd.FD_ERR_UNSUPPORTED
     assert fd.fd_page_tables(d, **{**a, "cu_tokens": None, "positions": None}) == fd.FD_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ arrays of the other page calls
+@pytest.mark.parametrize("op", ["fork", "trim", "compact"])
+def test_page_calls_refuse_arrays_of_other_sizes(fd, op):
+    i = lambda n: torch.zeros(n, dtype=torch.int32)
+    table, free, src = i(24).view(3, 8), i(9), i(3)
+    d = fd.make_page_desc(table, free, None, copies=src, page_size=16, n_pages=9)
+    good = dict(seqlens=i(3), free_pages=free, free_count=i(1), block_table=table, shares=i(9), free_count_out=i(1), copy_src=src, copy_dst=i(3),
+                copy_count=i(1), stream=0)
+    if op == "fork":
+        good.update(parents=i(2), children=i(2), keep=None, seqlens_out=i(3))
+    elif op == "trim":
+        good.update(keep=i(3), seqlens_out=i(3))
+    else:
+        good["n_keep"] = 4
+    call = getattr(fd, "fd_page_" + op)
+    bad = [("free_pages", i(8)), ("free_pages", i(9).long()), ("free_count", i(0)), ("free_count", i(1).long()), ("block_table", i(23)),
+           ("block_table", table.long()), ("block_table", i(48).view(3, 16)[:, :8]), ("shares", i(8)), ("shares", i(18)[::2]), ("free_count_out", i(0)),
+           ("free_count_out", i(1).float()), ("copy_src", i(2)), ("copy_src", i(3).long()), ("copy_dst", i(2)), ("copy_count", i(0)),
+           ("copy_count", i(1).long())]
+    for n, v in bad:
+        with pytest.raises(ValueError):
+            call(d, **{**good, n: v})
+    d.page_size = 4         # (refused by the library)
+    assert call(d, **good) == fd.FD_ERR_UNSUPPORTED
+
+
+def test_copy_refuses_counts_of_other_types(fd):
+    one = (fd.FdPool * 1)(pool(fd))
+    one.n_pages = 9
+    for count in (torch.zeros(1, dtype=torch.int64), torch.zeros(0, dtype=torch.int32), torch.zeros(1)):
+        with pytest.raises(ValueError):
+            fd.fd_page_copy(one, torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), count, stream=0)
