@@ -140,6 +140,8 @@ class FdRopeDesc(ctypes.Structure):
             "q_w_stride_h", "k_w_stride_h", "kv_extent")),
         *((n, ctypes.c_int32) for n in ("page_size", "batch", "flags", "reserved")),
     ]
+    sizes = None            # make_rope_desc: bytes of a token's queries and of its keys, of a cache; the weights' type, and
+                            # how many there are for queries and keys (0: not used)
 
 
 class FdPool(ctypes.Structure):
@@ -280,13 +282,13 @@ def _check_scales(desc, scales: FdKvScales) -> None:
 
 
 _types = {}
-_int32 = None
+_int32 = _int64 = _float32 = None
 
 
 def _array(t, n: int, name: str, kind: str):
     """Address of n contiguous elements of the type, checked if t is a tensor (addresses and None go
     unchecked)."""
-    global _int32
+    global _int32, _int64, _float32
     if t is None:
         return None
     try:
@@ -296,14 +298,26 @@ def _array(t, n: int, name: str, kind: str):
     if not _types:
         import torch
         _types.update(int32=torch.int32, int64=torch.int64, float32=torch.float32)
-        _int32 = torch.int32
+        _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
     if dtype is not _types[kind] or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous {kind}")
     return t.data_ptr()
 
 
+def _flat(t, n: int, name: str, dtype, kind: str):
+    """_array, the short way (dtype: what kind names, None before the first call)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _array(t, n, name, kind)
+
+
 def _i32(t, n: int, name: str):
-    """_array of int32, the short way."""
+    """_flat of int32."""
     if t is None:
         return None
     try:
@@ -312,6 +326,18 @@ def _i32(t, n: int, name: str):
     except AttributeError:
         pass
     return _array(t, n, name, "int32")
+
+
+def _room(t, size: int, name: str):
+    """Address of a strided tensor that holds `size` bytes or more (addresses and None go unchecked)."""
+    if t is None:
+        return None
+    try:
+        if t.nbytes >= size:
+            return t.data_ptr()
+    except AttributeError:
+        return _ptr(t)
+    raise ValueError(f"{name} must hold {size} bytes, as its descriptor says")
 
 
 def check(status: int, what: str = "") -> int:
@@ -441,7 +467,7 @@ def fd_page_tables(desc: FdPageDesc, seqlens, new_tokens, free_pages, free_count
                                   _i32(free_pages, desc.n_free_max, "free_pages"), _i32(free_count, 1, "free_count"),
                                   _i32(block_table, b * desc.max_pages_per_seq, "block_table"), _i32(seqlens_out, b, "seqlens_out"),
                                   _i32(free_count_out, 1, "free_count_out"), _i32(cu_tokens, b + 1, "cu_tokens"),
-                                  _array(slots, n, "slots", "int64"), _i32(positions, n, "positions"), _stream(stream))
+                                  _flat(slots, n, "slots", _int64, "int64"), _i32(positions, n, "positions"), _stream(stream))
 
 
 def fd_prompt_workspace_size(desc: FdPromptDesc) -> int:
@@ -461,9 +487,22 @@ def fd_qkv_rope(desc: FdRopeDesc, q, k, v, q_weight, k_weight, inv_freq, positio
                 v_cache, stream=None) -> int:
     """Norms and rotation of a step's queries and keys, and the way of its keys and values into a cache."""
     n = desc.n_tokens
-    return _load().fd_qkv_rope(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
-                               _array(inv_freq, desc.rot_dim // 2, "inv_freq", "float32"), _array(positions, n, "positions", "int32"),
-                               _array(slots, n, "slots", "int64"), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _stream(stream))
+    if desc.sizes is None:              # a descriptor of the caller's own: as for addresses
+        q_row = k_row = cache = 0
+    else:
+        q_row, k_row, cache, kind, q_weights, k_weights = desc.sizes
+        q_row, k_row = n * q_row, n * k_row
+        try:
+            if ((q_weight is not None and q_weights and (q_weight.dtype is not kind or q_weight.numel() < q_weights)) or
+                    (k_weight is not None and k_weights and (k_weight.dtype is not kind or k_weight.numel() < k_weights))):
+                raise ValueError("q_weight and k_weight must have the type and size of their descriptor's weights")
+        except AttributeError:
+            pass
+    return _load().fd_qkv_rope(ctypes.byref(desc), _room(q, q_row, "q"), _room(k, k_row, "k"), _room(v, k_row if cache else 0, "v"),
+                               _ptr(q_weight), _ptr(k_weight), _flat(inv_freq, desc.rot_dim // 2, "inv_freq", _float32, "float32"),
+                               _i32(positions, n, "positions"), _flat(slots, n, "slots", _int64, "int64"), _room(q_out, q_row, "q_out"),
+                               _room(k_out, k_row, "k_out"), _room(k_cache, cache, "k_cache"), _room(v_cache, cache, "v_cache"),
+                               _stream(stream))
 
 
 def _page_arrays(desc, free_pages, free_count, block_table, shares, free_count_out, copy_src, copy_dst, copy_count):
@@ -652,6 +691,7 @@ def make_rope_desc(q, k, v=None, *, q_out=None, k_out=None, k_cache=None, v_cach
     whole 16-byte rows; q or k may be None), rows out q_out and k_out of their shapes, caches
     [P, Hkv, page, D] (paged) or [B, Hkv, T, D] (page_size 0) of their type or float8_e4m3fn,
     and weights [D] or [heads, D]."""
+    import torch
     d = FdRopeDesc()
     x = q if q is not None else k
     if x is None:
@@ -710,6 +750,10 @@ def make_rope_desc(q, k, v=None, *, q_out=None, k_out=None, k_cache=None, v_cach
         d.w_dtype = _dtype_code(w.dtype)
     if len(types) > 1:
         raise ValueError("q_weight and k_weight must have one type")
+    count = lambda used, heads, stride: 0 if not used else d.head_dim * (heads if stride else 1)
+    d.sizes = (2 * d.head_dim * d.n_q_heads, 2 * d.head_dim * d.n_kv_heads, 0 if k_cache is None else k_cache.nbytes,
+               types.pop() if types else torch.float32, count(d.norm & FD_NORM_Q, d.n_q_heads, d.q_w_stride_h),
+               count(d.norm & FD_NORM_K, d.n_kv_heads, d.k_w_stride_h))
     d.rot_dim, d.interleaved = int(rot_dim), int(bool(interleaved))
     d.eps, d.rot_scale, d.k_scale, d.v_scale = float(eps), float(rot_scale), float(k_scale), float(v_scale)
     d.flags = d.reserved = 0

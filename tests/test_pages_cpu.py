@@ -301,3 +301,44 @@ def test_copy_refuses_counts_of_other_types(fd):
     for count in (torch.zeros(1, dtype=torch.int64), torch.zeros(0, dtype=torch.int32), torch.zeros(1)):
         with pytest.raises(ValueError):
             fd.fd_page_copy(one, torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), count, stream=0)
+
+
+# ------------------------------------------------------------------ tensors of fd_qkv_rope
+def test_rope_refuses_weights_that_are_not_its_descriptors(fd):
+    """A descriptor without weights says 32 bits: bf16 ones would be read behind their end."""
+    x = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    pos, freq, w = torch.zeros(3, dtype=torch.int32), torch.zeros(64), torch.zeros(128, dtype=torch.bfloat16)
+    call = lambda d, qw, kw: fd.fd_qkv_rope(d, x, x, None, qw, kw, freq, pos, None, x, x, None, None, 0)
+    bare = fd.make_rope_desc(x, x, q_out=x, k_out=x)
+    shared = fd.make_rope_desc(x, x, q_out=x, k_out=x, q_weight=w, k_weight=w)
+    per_head = fd.make_rope_desc(x, x, q_out=x, k_out=x, q_weight=w.expand(4, 128).clone(), k_weight=w.expand(4, 128).clone())
+    for d, qw, kw in ((bare, w, None), (bare, None, w), (bare, torch.zeros(64), None), (shared, w.float(), w), (shared, w, w.half()), (shared, w[:64], w),
+                      (per_head, w, None), (per_head, None, torch.zeros(3, 128, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            call(d, qw, kw)
+    for d in (bare, shared, per_head):
+        d.rot_dim = 24              # (refused by the library, so that nothing reaches a GPU here)
+    assert call(shared, w, w) == call(shared, w, None) == call(shared, None, None) == call(bare, torch.zeros(128), None) == fd.FD_ERR_UNSUPPORTED
+    assert call(per_head, torch.zeros(4, 128, dtype=torch.bfloat16), None) == fd.FD_ERR_UNSUPPORTED
+    none = fd.make_rope_desc(x, x, q_out=x, k_out=x, norm_q=False, norm_k=False)
+    none.rot_dim = 24
+    assert call(none, w, w) == fd.FD_ERR_UNSUPPORTED          # no norm: weights are not read
+
+
+def test_rope_refuses_tensors_that_are_smaller_than_its_descriptor_says(fd):
+    x = torch.zeros(6, 8, 128, dtype=torch.float16)
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    pos, freq, slots = torch.zeros(6, dtype=torch.int32), torch.zeros(64), torch.zeros(6, dtype=torch.int64)
+    qo, ko = torch.zeros(6, 4, 128, dtype=torch.float16), torch.zeros(6, 2, 128, dtype=torch.float16)
+    for page in (16, 0):
+        kc, vc = (torch.zeros(5, 2, 16, 128, dtype=torch.float16) for _ in range(2))
+        d = fd.make_rope_desc(q, k, v, q_out=qo, k_out=ko, k_cache=kc, v_cache=vc, page_size=page)
+        good = dict(q=q, k=k, v=v, q_weight=None, k_weight=None, inv_freq=freq, positions=pos, slots=slots, q_out=qo, k_out=ko, k_cache=kc, v_cache=vc,
+                    stream=0)
+        for n, t in (("q", q[:5]), ("k", k[:, :1]), ("v", v[1:]), ("q_out", qo[:, :3]), ("k_out", ko[:5]), ("k_cache", kc[:4]),
+                     ("v_cache", vc.to(torch.float8_e4m3fn)), ("v_cache", vc[:, :, :8])):
+            with pytest.raises(ValueError):
+                fd.fd_qkv_rope(d, **{**good, n: t})
+        d.rot_dim = 24
+        assert fd.fd_qkv_rope(d, **good) == fd.FD_ERR_UNSUPPORTED
+        assert fd.fd_qkv_rope(d, **{**good, "k_out": None}) == fd.FD_ERR_UNSUPPORTED
