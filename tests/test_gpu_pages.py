@@ -733,3 +733,128 @@ def test_copies_of_several_shapes_behind_forks_and_trims(captured):
         wrong += (lens2 != i32(out["lens"])).sum() + (table != i32(out["table"])).sum()
     assert int(wrong) == 0
     assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+# ------------------------------------------------------------------ long rows: stages in turn, last pieces, rows apart
+LONG = {    # pools, their tensors' shape behind the pages, the part that the k-th pool is, rows of a page, pieces of a row
+    "pages of 32 KB": (64, (8, 32, 128), lambda k, x: x, 1, 2),
+    "16400": (40, (16400,), lambda k, x: x, 1, 2),                                          # a last piece of 16 bytes
+    "40976, apart": (12, (3, 41024), lambda k, x: x[:, :, :40976], 3, 3),                   # one of 8208, 48 bytes between the rows
+    "8208, apart in two dimensions": (6, (4, 6, 8256), lambda k, x: x[:, :3, :5, :8208] if k % 2 else x.permute(0, 2, 1, 3)[:, :5, :3, :8208], 15, 1),
+    "8192, heads ahead of pages": (14, (5, 8192), lambda k, x: x.view(5, -1, 8192).permute(1, 0, 2), 5, 1),
+}
+
+
+@pytest.mark.parametrize("name", sorted(LONG))
+def test_copy_of_long_rows(name):
+    """Thirteen pieces and more for each of the CTAs (two an SM), so that every stage is used again and again;
+    pairs are left out among them, and what lies between the rows stays."""
+    n, shape, part, rows, pieces = LONG[name]
+    P, pairs = 190, 90
+    back = [rand_bytes(300 + k, torch.uint8, P, *shape) for k in range(n)]
+    before = [x.clone() for x in back]
+    perm = [int(x) for x in np.random.default_rng(n).permutation(P)]
+    src, dst = perm[:pairs], perm[pairs:2 * pairs]
+    for k in range(0, pairs, 7):
+        src[k] = src[1]
+    for k in range(3, pairs, 11):
+        dst[k] = -1
+    dst[50] = src[50]
+    counted = [(a, b) for a, b in zip(src, dst) if b >= 0 and a != b][:pairs]
+    assert len(counted) * n * rows * pieces >= 13 * 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    pools = fd.make_pools([part(k, x) for k, x in enumerate(back)])
+    fd.check(fd.fd_page_copy(pools, i32(src), i32(dst)))
+    for k, (x, y) in enumerate(zip(back, before)):
+        old, new = part(k, y).clone(), part(k, y)
+        for a, b in counted:
+            new[b] = old[a]
+        assert torch.equal(x, y), k
+    fd.check(fd.fd_page_copy(pools, i32(dst), i32([-1] * 40 + src[40:]), i32([40])))        # a count that ends ahead of what counts
+    for x, y in zip(back, before):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("row", [32768, 4096, 72])
+def test_copy_beyond_32_bit_offsets(row):
+    """Pages behind 2^31 and 2^32 bytes of a pool, by bulk copies and by registers."""
+    P = (1 << 32) // row + 1000
+    x = torch.zeros(P, row, dtype=torch.uint8, device=DEV)
+    places = [3, (1 << 31) // row - 1, (1 << 31) // row + 5, (1 << 32) // row - 1, (1 << 32) // row + 7, P - 1, P - 2, 11]
+    for k, q in enumerate(places):
+        x[q] = rand_bytes(400 + k, torch.uint8, row)
+    rows = [x[q].clone() for q in places]
+    to = [P - 3, 5, P - 500, (1 << 31) // row + 9, 7, (1 << 32) // row + 2, (1 << 31) // row - 7, (1 << 32) // row - 9]
+    fd.check(fd.fd_page_copy(fd.make_pools([x]), i32(places), i32(to)))
+    for k in range(len(to)):
+        assert torch.equal(x[to[k]], rows[k]) and torch.equal(x[places[k]], rows[k])
+        x[to[k]] = 0
+        x[places[k]] = 0
+    assert int(x.view(-1).view(torch.int64).count_nonzero()) == 0       # (and nothing else was written)
+
+
+# ------------------------------------------------------------------ trims that lack pages; large calls in a graph
+@pytest.mark.parametrize("batch,width", [(600, 5), (3000, 12), (8192, 4)])
+@pytest.mark.parametrize("count", [0, 9, 80])
+def test_trim_that_lacks_pages_of_more_sequences_than_threads(batch, width, count):
+    """More claims than free pages, numbered over several rounds of a CTA's threads."""
+    s = shared_state(batch + count, batch, 16, width, batch // 3)
+    keep = random_keep(s, s.r)
+    claims = sum(1 for b, k in enumerate(keep) if 0 <= k < s.lens[b] and k % 16)
+    s.count = min(s.count, count)
+    want, bad = want_trim(s, keep)
+    assert claims > s.count and bad
+    same(run_trim(s, keep), want, True)
+
+
+def test_large_trims_and_compactions_captured():
+    """Sixteen CTAs each (more table entries than eight take), one graph over other lengths and tables."""
+    batch, page, width, n_pages = 400, 16, 120, 30000
+    states = []
+    for seed in range(3):
+        s = State(500 + seed, batch, page, width, held=0.6, spare=0)
+        perm = [int(x) for x in s.r.permutation(n_pages)]
+        have = [-(-x // page) for x in s.lens]
+        at = np.concatenate([[0], np.cumsum(have)])
+        assert at[-1] < n_pages - 2000
+        s.n_pages, s.shares = n_pages, [0] * n_pages
+        s.table = [perm[at[b]:at[b + 1]] + [-9] * (width - have[b]) for b in range(batch)]
+        s.free = perm[at[-1]:]
+        s.count = len(s.free)
+        s.free += [-5] * (n_pages - s.count)
+        out, bad = want_fork(s, *s.forked(100))
+        assert not bad
+        s.take(out)
+        keep = random_keep(s, s.r)
+        given = dict(lens=s.lens, count=[s.count], table=s.table, free=s.free, shares=s.shares, cut=keep)
+        trimmed, bad = ref.trim(keep, s.lens, s.free, s.count, s.table, s.shares, page, n_pages, [77] * n_pages, [78] * n_pages)
+        assert not bad
+        s.take(trimmed)
+        n_keep = n_pages // 2
+        packed, bad = ref.compact(n_keep, s.lens, s.free, s.count, s.table, s.shares, page, n_pages, trimmed["src"], trimmed["dst"])
+        assert not bad and packed["n"] > 1000
+        states.append(({k: i32(v) for k, v in given.items()}, trimmed, packed))
+    now = {k: v.clone() for k, v in states[0][0].items()}
+    table = now["table"].view(batch, width)
+    src, dst = i32([77] * n_pages), i32([78] * n_pages)
+    n1, n2, lens2, count2, count3 = i32([0]), i32([0]), torch.zeros_like(now["lens"]), i32([0]), i32([0])
+    desc = fd.make_page_desc(table, now["free"], None, copies=src, page_size=page, n_pages=n_pages)
+
+    def step():
+        fd.check(fd.fd_page_trim(desc, now["cut"], now["lens"], now["free"], now["count"], table, now["shares"], lens2, count2, src, dst, n1))
+        fd.check(fd.fd_page_compact(desc, n_pages // 2, lens2, now["free"], count2, table, now["shares"], count3, src, dst, n2))
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for given, trimmed, packed in states * 2:
+        for k, v in given.items():
+            now[k].copy_(v)
+        src.fill_(77), dst.fill_(78)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert lens2.tolist() == trimmed["lens"] and int(count2) == trimmed["count"] and int(n1) == trimmed["n"]
+        assert table.tolist() == packed["table"] and now["shares"].tolist() == packed["shares"] and now["free"].tolist() == packed["free"]
+        assert int(count3) == packed["count"] and int(n2) == packed["n"]
+        assert src.tolist() == packed["src"] and dst.tolist() == packed["dst"]
+    assert fd.fd_device_status(clear=True) == fd.FD_OK

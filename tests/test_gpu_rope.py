@@ -351,3 +351,20 @@ def test_e4m3_of_large_finite_values(n, scale):
     want = [math.copysign(448.0, math.cos(a)), math.copysign(448.0, math.sin(a))]
     assert [float(turned[3]), float(turned[3 + 32])] == want
     assert int(torch.isnan(s.kc.float()).sum()) == 2 and int(torch.isnan(s.vc.float()).sum()) == 2
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_rows_beyond_32_bit_offsets(pairs):
+    """Queries and keys, in and out, of more than 2^31 elements each."""
+    n, h = (1 << 31) // (16 * D) + 1500, 16
+    s = Step(23, 1, h, h, "bf16", "none", pairs=pairs)
+    block = (torch.randn(5000, h, D, generator=gen(24), device=DEV) * 2).to(s.T)
+    x = block.repeat(-(-n // 5000), 1, 1)[:n]
+    pos = torch.randint(0, 100000, (n,), generator=gen(25), device=DEV, dtype=torch.int32)
+    q_out, k_out = torch.zeros_like(x), torch.zeros_like(x)
+    d = fd.make_rope_desc(x, x, q_out=q_out, k_out=k_out, q_weight=s.qw, k_weight=s.kw, interleaved=pairs)
+    fd.check(fd.fd_qkv_rope(d, x, x, None, s.qw, s.kw, s.freq, pos, None, q_out, k_out, None, None))
+    for a, b in ((0, 300), (n // 2 - 100, n // 2 + 100), (n - 1700, n)):
+        for got, w in ((q_out, s.qw), (k_out, s.kw)):
+            want, err = ref.rope(x[a:b], w, True, pos[a:b], s.freq.tolist(), 128, pairs, s.eps, 1.0)
+            ref.close(got[a:b], want, err + ref.rounding(want, s.T), (a, b))
