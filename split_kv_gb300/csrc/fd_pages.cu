@@ -4,11 +4,12 @@
 //
 // Nothing here is bound by bandwidth (4 to 28 bytes per page); the time is the
 // chain of dependent reads, atomics and barriers.  So what CTAs have to agree on
-// each computes for itself (prefix sums over the sequences or forks), and where
-// that is not enough the call is one cluster, whose CTAs write into each
-// other's shared memory (counts, the bitmap of held pages) and meet at
-// the hardware's cluster barrier: one launch, no spin, no workspace.  Outputs that
-// may alias inputs are written behind every CTA's reads of them.
+// each computes for itself (prefix sums over the sequences or forks): that is all
+// a fork needs, which runs on the whole grid.  Trims and compactions need more and are one
+// cluster, whose CTAs write into each other's shared memory (counts, ranges of the bitmap of
+// held pages) and meet at the hardware's cluster barrier: one launch, no spin, no
+// workspace.  Outputs that may alias inputs are written behind every CTA's reads of
+// them: behind a barrier of the cluster, and by a fork of more than one CTA in a second launch.
 //
 // Which page gets what never depends on the order of atomics: a trim's sequences
 // and pages are numbered, and the largest number wins by an atomic minimum of its code.
