@@ -563,11 +563,12 @@ typedef struct fd_rope_desc {
  *               overlap it).  k_out may be NULL.
  *  k_cache, v_cache : device, both or neither.
  * Arithmetic: norms and rotation in 32 bits (sums of squares too: they overflow
- * for values of about 1.6e18), angles as fractions of a turn in 64-bit fixed
- * point, so that they are as exact for far positions as for near ones; each
- * result is rounded once to its output's type.  FD_E4M3: the value times the
- * reciprocal of the scale (rounded to 32 bits), to the nearest, ties to even,
- * beyond 448 to 448; an infinity or NaN is stored as NaN. */
+ * for values of about 1.6e18 and, with eps 0, lose bits for rows below about 1e-19),
+ * angles as fractions of a turn in 64-bit fixed point, so that they are as exact for
+ * far positions as for near ones; each result is rounded once to its output's type.
+ * FD_E4M3: the value times the reciprocal of the scale (rounded to 32 bits), to the
+ * nearest, ties to even, beyond 448 to 448; a value that is an infinity or NaN ahead of
+ * the scale is stored as NaN. */
 fd_status fd_qkv_rope(const fd_rope_desc* desc, const void* q, const void* k, const void* v,
                       const void* q_weight, const void* k_weight, const float* inv_freq,
                       const int32_t* positions, const int64_t* slots, void* q_out, void* k_out,
@@ -643,9 +644,15 @@ fd_status fd_page_trim(const fd_page_desc* desc, const int32_t* keep, const int3
  *  n_keep   : 0 <= n_keep <= n_pages.
  *  seqlens  : device int32[batch].
  *  shares   : device int32[n_pages], in and out; NULL: no page is shared.
- * Pages that F or the copy list cannot take stay where they are.  Those, a
- * length out of range (its table entries are left as they are), a page index
- * outside the pool and a free count out of range set FD_ERR_DEVICE_BOUNDS in the status word. */
+ * Pages that F or the copy list cannot take stay where they are, while the free ones
+ * from n_keep on leave the stack all the same.  None stays while the pages held are
+ * n_keep at most, every other page is in the stack, and n_slots is n_pages - n_keep or
+ * more.  A caller that goes on with the high end after all puts back what is free of
+ * it: the entries from n_keep on of a copy of free_pages (its first free_count)
+ * that it kept from before the call, and copy_src.
+ * Pages that stay, a length out of range (its table entries are left as they are), a
+ * page index outside the pool and a free count out of range set FD_ERR_DEVICE_BOUNDS in
+ * the status word. */
 fd_status fd_page_compact(const fd_page_desc* desc, int32_t n_keep, const int32_t* seqlens,
                           int32_t* free_pages, const int32_t* free_count, int32_t* block_table,
                           int32_t* shares, int32_t* free_count_out, int32_t* copy_src,

@@ -13,8 +13,9 @@
 // Angles: a turn is 2^64.  inv_freq / 2 pi is made a 64-bit fraction once per
 // thread (24 bits of inv_freq times 2^64 / 2 pi, shifted), position times
 // that, modulo 2^64, is the angle with the whole turns gone: one integer
-// product, as exact for position 10^6 as for 1 (an error of 2^-32 of a turn from
-// the bits that the conversion to 32-bit floats leaves).  The sines and
+// product, as exact for position 10^6 as for 1.  Its upper half becomes a 32-bit float of
+// half turns: the cut is off by up to 2^-32 of a turn, the conversion by up to 2^-26 (half a
+// step next to half a turn, about 1e-7 radians).  The sines and
 // cosines of a token are shared by the rows of an item: each of a warp's four
 // row groups computes a quarter of them.
 #include <algorithm>

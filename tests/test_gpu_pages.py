@@ -858,3 +858,23 @@ def test_large_trims_and_compactions_captured():
         assert int(count3) == packed["count"] and int(n2) == packed["n"]
         assert src.tolist() == packed["src"] and dst.tolist() == packed["dst"]
     assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+@pytest.mark.parametrize("part,lists", [(0.3, None), (0.8, 5), (0.9, 5), (0.9, None)])
+def test_compact_and_the_high_end_kept_after_all(part, lists):
+    """The stack as it was, from n_keep on, and the pages that moved are what is free of the high end: with
+    them no page is lost, whether the compaction could finish or not."""
+    s = shared_state(71, 60, 16, 30, 20)
+    n_keep = int(s.n_pages * part)
+    n_lists = s.n_pages if lists is None else lists
+    held = {p for b, x in enumerate(s.lens) for p in s.table[b][:-(-x // 16)]}
+    fits = len(held) <= n_keep and n_lists >= s.n_pages - n_keep
+    kept = [p for p in s.free[:s.count] if p >= n_keep]
+    want, bad = want_compact(s, n_keep, n_lists)
+    assert bad == (not fits)
+    t = run_compact(s, n_keep, n_lists)
+    same(t, want, bad)
+    table, n = t["table"].tolist(), int(t["n"])
+    held = {p for b, x in enumerate(s.lens) for p in table[b][:-(-x // 16)]}
+    free = t["free"].tolist()[:int(t["count_out"])] + kept + t["src"].tolist()[:n]
+    assert len(free) == len(set(free)) and not held & set(free) and held | set(free) == set(range(s.n_pages))
