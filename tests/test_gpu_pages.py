@@ -664,7 +664,7 @@ def test_copy_of_pools_in_any_order(layers):
 @pytest.mark.parametrize("captured", [False, True])
 def test_copies_of_several_shapes_behind_forks_and_trims(captured):
     """Lists that a fork and a trim write directly ahead of the copies, over and over: every launch of a
-    copy sees the list of the call before it, not that of the round before, and its pages."""
+    copy sees the list of the call before it, not that of the repetition before, and its pages."""
     states = []
     for seed in range(2):
         s = State(90 + seed, 40, 16, 12, held=0.6, spare=200, empty=12)
